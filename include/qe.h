@@ -61,7 +61,8 @@ typedef enum { QE_F32 = 0, QE_BF16 = 1 } qe_dtype;
  *   d_in, d_out  input / output channels (d_in > 0, d_out > 0)
  *   w_bits       4 (int4, per-output-channel symmetric) or 3 (3-bit, weight-only)
  *   a_bits       6 or 8 (per-token symmetric activation codes) with w_bits 4;
- *                16 (bf16 activations, no activation quantization) with w_bits 3 or 4
+ *                16 (bf16 activations, no activation quantization) with w_bits 3 or 4;
+ *                4 with w_bits 4: microscaled 4-bit floating point on both sides (below)
  *   r_shared     shared-expert rank, 0..64 (0 = no shared expert)
  *   n_routed     number of routed experts N_r, 0..16 (0 = no router, no routed expert)
  *   r_routed     routed-expert rank, 1..64 when n_routed > 0, else 0
@@ -295,6 +296,72 @@ int qe_group_gemm(const qe_linear* const* lins, int32_t n_lin, const int8_t* con
 size_t qe_noalloc_scratch_bytes(void);
 int qe_linear_forward_noalloc(const qe_linear* lin, const void* x, int32_t x_dtype, int32_t T, float* y,
                               int32_t* expert_out, void* stream);
+
+/* --------------------------------------------- microscaled 4-bit floating point --
+ * The QE linear with its main product in microscaled 4-bit floating point (the OCP Microscaling
+ * Formats specification, version 1.0, type MXFP4), in place of the integer codes of the W4A6 / W4A8
+ * settings: y = Q(x / s) . Q(W_f diag(s))^T + (x . A_s) . B_s + (x . A_e) . B_e as above (DeepRead
+ * summary, "Method"), with Q the block quantization below on both operands, which the matrix cores
+ * multiply without unpacking.
+ *
+ * Form of a [T][d] tensor: blocks of 32 consecutive channels share a scale.
+ *   codes   uint8 [T][d/2]: channel 2m in bits 0-3, 2m+1 in bits 4-7 of byte m; bit 3 the sign,
+ *           bits 0-2 index 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  uint8 [T][d/32]: the block's scale is 2^(byte - 127); 255 is NaN
+ * Quantization of a block with largest magnitude amax: byte = floor(log2 amax) - 2 + 127, at least 0
+ * (0 for a zero block); code = the nearest entry to |value| / scale, a value halfway between two
+ * taking the even index, values above 6 taking 6.  A block that holds a NaN or an infinity gets byte
+ * 255 and zero codes, so it reads back as NaN and makes the products that use it NaN.
+ *
+ * qe_mx4_quant: codes and scales of x / smooth (multiply 0: activations) or x * smooth (multiply 1:
+ *   weights), in float32 with IEEE division; smooth NULL: of x.  x device [T][d] (x_dtype), smooth device
+ *   float32 [d] (entries > 0), codes and scales device as above.  d % 32 == 0 (else QE_ERR_UNSUPPORTED).
+ * qe_mx4_dequant: x = the values of codes and scales (exact in both types; rounded to nearest even
+ *   where they lie below bf16's smallest step).  x device [T][d] (x_dtype).
+ * qe_mx4_prepare: qe_prepare for a linear with a_bits 4: w_codes and w_scales are the canonical form of
+ *   its [d_out][d_in] weights (qe_mx4_quant of W_f with multiply 1); the other arguments as there.
+ * qe_mx4_gemm: the main product with both low-rank terms (qe_wq_gemm's counterpart):
+ *     y[t][i] = sum_j a[t][j] w[i][j] + u[t] . B_s[:, i] + v[t] . B_{expert[t]}[:, i]
+ *   with a the values of codes / scales (device, [T][d_in] in the form above, e.g. from qe_mx4_quant or
+ *   qe_add_rmsnorm), w the prepared weights, exact products and float32 sums.  u, v, expert, perm as for
+ *   qe_wq_gemm (u NULL: no shared term; v and expert NULL: no routed term; expert entries are clamped to
+ *   [0, n_routed); perm, when given, is a permutation of the tokens: it changes the schedule and not
+ *   the results).  y: device [T][d_out], y_dtype.  Few tokens or channels: the K steps may be split over
+ *   workgroups, whose float32 partials lie in the workspace and are added in order.  Deterministic.
+ * qe_linear_forward, qe_linear_forward_noalloc, qe_group_forward, qe_linear_forward_top2, qe_route,
+ * qe_adapter_inputs, qe_routed_lora, qe_linear_cost and the sizing calls take linears with a_bits 4;
+ * qe_prepare, qe_linear_prologue, qe_group_prologue, qe_wq_gemm and qe_group_gemm, whose arguments are
+ * integer codes, return QE_ERR_UNSUPPORTED for them.
+ */
+int qe_mx4_quant(const void* x, int32_t x_dtype, const float* smooth, int32_t multiply, int32_t T, int32_t d,
+                 uint8_t* codes, uint8_t* scales, void* stream);
+int qe_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int32_t T, int32_t d, void* x, int32_t x_dtype,
+                   void* stream);
+int qe_mx4_prepare(const qe_linear* lin, const uint8_t* w_codes, const uint8_t* w_scales, const float* smooth,
+                   const uint16_t* A_s, const uint16_t* B_s, const uint16_t* A_r, const uint16_t* B_r,
+                   const uint16_t* R, void* prep, void* stream);
+int qe_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_t* scales, int32_t T, const uint16_t* u,
+                const uint16_t* v, const int32_t* expert, const int32_t* perm, float* y, void* ws, size_t ws_bytes,
+                void* stream);
+
+/* -------------------------------------------------- residual addition and RMS norm --
+ * What stands between two quantized linears of a decoder layer, with the next one's activation codes
+ * made in the same pass (qe_quant_act's and qe_mx4_quant's place when the input comes from a norm):
+ *   h  = rn(x + res)  (res NULL: h = x)
+ *   r  = float32(1 / sqrt(sum_j h[j]^2 / d + eps)), with the sum, the root and the quotient in float64
+ *   xn = rn((h * r) * weight), the products in float32
+ *   a_bits 6, 8: codes (int8 [T][d]) and scales (float32 [T]) as qe_quant_act(xn, smooth) gives them
+ *   a_bits 4: codes (uint8 [T][d/2]) and scales (uint8 [T][d/32]) as qe_mx4_quant(xn, smooth) does
+ *   a_bits 0: no codes (smooth, codes and scales NULL)
+ * with rn the rounding to x_dtype (nearest even).  x, res, h, xn: device [T][d] of x_dtype; weight: device
+ * [d] of weight_dtype; smooth: device float32 [d] (entries > 0) or NULL.  h, xn: NULL when not wanted (at
+ * least one of h, xn and codes is).  In place: h or xn may be x or res itself (both may not be one
+ * buffer); no other overlap.  eps > 0.  d % 8 == 0 (d % 32 == 0 for a_bits 4) and d <= 32768, else
+ * QE_ERR_UNSUPPORTED.
+ */
+int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* weight, int32_t weight_dtype,
+                   float eps, int32_t T, int32_t d, void* h, void* xn, const float* smooth, int32_t a_bits, void* codes,
+                   void* scales, void* stream);
 
 /* ------------------------------------------------- channel-importance statistic --
  * (a8 helper) w[j] = (sum_i |W[i][j]|) / d_out: the column mean of |W_f|, one value

@@ -71,6 +71,11 @@ def _load():
         "qe_group_gemm": (ctypes.c_int, [P, I, P, P, I, P, P, P, P, P, P, P, P]),
         "qe_noalloc_scratch_bytes": (Z, []),
         "qe_linear_forward_noalloc": (ctypes.c_int, [LP, P, I, I, P, P, P]),
+        "qe_mx4_quant": (ctypes.c_int, [P, I, P, I, I, I, P, P, P]),
+        "qe_mx4_dequant": (ctypes.c_int, [P, P, I, I, P, I, P]),
+        "qe_mx4_prepare": (ctypes.c_int, [LP, P, P, P, P, P, P, P, P, P, P]),
+        "qe_mx4_gemm": (ctypes.c_int, [LP, P, P, I, P, P, P, P, P, P, Z, P]),
+        "qe_add_rmsnorm": (ctypes.c_int, [P, P, I, P, I, ctypes.c_float, I, I, P, P, P, I, P, P, P]),
         "qe_colmean_abs": (ctypes.c_int, [P, I, I, I, P, P]),
         "qe_channel_topk": (ctypes.c_int, [P, I, P, I, I, I, P, P, P]),
         "qe_partition_channels": (ctypes.c_int, [P, I, I, I, P, P, P]),
@@ -121,7 +126,7 @@ EXPORTED = (
     "qe_sub_lowrank", "qe_lowrank_workspace_bytes", "qe_lowrank_fit", "qe_build_experts_workspace_bytes",
     "qe_build_experts", "qe_lowrank_cov_workspace_bytes", "qe_lowrank_fit_cov",
     "qe_build_experts_cov_workspace_bytes", "qe_build_experts_cov", "qe_router_targets_workspace_bytes", "qe_router_targets", "qe_router_fit_workspace_bytes",
-    "qe_router_fit",
+    "qe_router_fit", "qe_mx4_quant", "qe_mx4_dequant", "qe_mx4_prepare", "qe_mx4_gemm", "qe_add_rmsnorm",
 )
 
 
@@ -289,6 +294,105 @@ def qe_linear_forward_noalloc(lin, x, y, expert_out, stream=None):
     """qe_linear_forward with the library's per-GPU scratch array as its workspace."""
     _check(_lib.qe_linear_forward_noalloc(ctypes.byref(lin), _ptr(x), _dtype_code(x), x.shape[0], _ptr(y),
                                           _ptr(expert_out), _stream(stream)), "qe_linear_forward_noalloc")
+
+
+def _on(where, first, *rest):
+    """Checks the arguments of a device call: (name, tensor, shape, dtype) each, tensor None where it
+    may be left out; all dense, on the device of the first.  Returns that device's index."""
+    dev = first[1].device
+    for name, t, shape, dtype in (first, *rest):
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{where}: {name} must have shape {shape}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        if t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, not {dev}")
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: needs device tensors, got {dev}")
+    return dev.index
+
+
+def _call_on(index, where, fn, *args, stream=None):
+    """fn(*args, stream) with the tensors' device current, on `stream` or that device's current one."""
+    import torch
+    if index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(stream))
+    _check(st, where)
+
+
+def qe_mx4_quant(x, smooth, codes, scales, multiply=False, stream=None):
+    """Enqueue the microscaled 4-bit form of x / smooth (multiply: x * smooth; smooth may be None):
+    codes uint8 [T, d // 2], scales uint8 [T, d // 32]."""
+    import torch
+    T, d = x.shape
+    dev = _on("qe_mx4_quant", ("x", x, (T, d), x.dtype), ("smooth", smooth, (d,), torch.float32),
+              ("codes", codes, (T, d // 2), torch.uint8), ("scales", scales, (T, d // 32), torch.uint8))
+    _call_on(dev, "qe_mx4_quant", _lib.qe_mx4_quant, _ptr(x), _dtype_code(x), _ptr(smooth), int(multiply), T, d,
+             _ptr(codes), _ptr(scales), stream=stream)
+
+
+def qe_mx4_dequant(codes, scales, x, stream=None):
+    """Enqueue x (bf16 or float32 [T, d]) = the values of microscaled codes and scales."""
+    import torch
+    T, d = x.shape
+    dev = _on("qe_mx4_dequant", ("x", x, (T, d), x.dtype), ("codes", codes, (T, d // 2), torch.uint8),
+              ("scales", scales, (T, d // 32), torch.uint8))
+    _call_on(dev, "qe_mx4_dequant", _lib.qe_mx4_dequant, _ptr(codes), _ptr(scales), T, d, _ptr(x), _dtype_code(x),
+             stream=stream)
+
+
+def qe_mx4_prepare(lin: qe_linear, w_codes, w_scales, smooth, A_s, B_s, A_r, B_r, R, prep, stream=None):
+    """qe_prepare for a linear with a_bits 4 (w_codes, w_scales: qe_mx4_quant of its weights)."""
+    import torch
+    bf, i, o, rs, n, rr = torch.bfloat16, lin.d_in, lin.d_out, lin.r_shared, lin.n_routed, lin.r_routed
+    dev = _on("qe_mx4_prepare", ("w_codes", w_codes, (o, i // 2), torch.uint8),
+              ("w_scales", w_scales, (o, i // 32), torch.uint8), ("smooth", smooth, (i,), torch.float32),
+              ("A_s", A_s, (i, rs), bf), ("B_s", B_s, (rs, o), bf), ("A_r", A_r, (n, i, rr), bf),
+              ("B_r", B_r, (n, rr, o), bf), ("R", R, (i, n), bf), ("prep", prep, tuple(prep.shape), torch.uint8))
+    need = qe_prepared_bytes(lin)
+    if prep.numel() < need:
+        raise ValueError(f"qe_mx4_prepare: prep holds {prep.numel()} bytes of {need}")
+    _call_on(dev, "qe_mx4_prepare", _lib.qe_mx4_prepare, ctypes.byref(lin), _ptr(w_codes), _ptr(w_scales),
+             _ptr(smooth), _ptr(A_s), _ptr(B_s), _ptr(A_r), _ptr(B_r), _ptr(R), _ptr(prep), stream=stream)
+
+
+def qe_mx4_gemm(lin: qe_linear, codes, scales, u, v, expert, y, ws, perm=None, stream=None):
+    """Enqueue y = the product of microscaled activations [T, d_in] and the prepared weights, plus the
+    shared (u) and routed (v, expert) low-rank terms where given (rows padded to rank_pad)."""
+    import torch
+    T = codes.shape[0]
+    dev = _on("qe_mx4_gemm", ("codes", codes, (T, lin.d_in // 2), torch.uint8),
+              ("scales", scales, (T, lin.d_in // 32), torch.uint8),
+              ("u", u, (T, rank_pad(lin.r_shared)), torch.bfloat16),
+              ("v", v, (T, rank_pad(lin.r_routed)), torch.bfloat16), ("expert", expert, (T,), torch.int32),
+              ("perm", perm, (T,), torch.int32),
+              ("y", y, (T, lin.d_out), torch.bfloat16 if lin.y_dtype == QE_BF16 else torch.float32),
+              ("ws", ws, tuple(ws.shape), ws.dtype))
+    _call_on(dev, "qe_mx4_gemm", _lib.qe_mx4_gemm, ctypes.byref(lin), _ptr(codes), _ptr(scales), T, _ptr(u), _ptr(v),
+             _ptr(expert), _ptr(perm), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), stream=stream)
+
+
+def qe_add_rmsnorm(x, res, weight, eps, h=None, xn=None, smooth=None, a_bits=0, codes=None, scales=None, stream=None):
+    """Enqueue h = x + res (res may be None), xn = RMS norm of h times weight, and with a_bits 4, 6 or 8
+    the codes and scales of xn / smooth (see include/qe.h; outputs left out are None)."""
+    import torch
+    T, d = x.shape
+    mx = a_bits == 4
+    dev = _on("qe_add_rmsnorm", ("x", x, (T, d), x.dtype), ("res", res, (T, d), x.dtype),
+              ("weight", weight, (d,), weight.dtype), ("h", h, (T, d), x.dtype), ("xn", xn, (T, d), x.dtype),
+              ("smooth", smooth, (d,), torch.float32),
+              ("codes", codes, (T, d // 2 if mx else d), torch.uint8 if mx else torch.int8),
+              ("scales", scales, (T, d // 32) if mx else (T,), torch.uint8 if mx else torch.float32))
+    _call_on(dev, "qe_add_rmsnorm", _lib.qe_add_rmsnorm, _ptr(x), _ptr(res), _dtype_code(x), _ptr(weight),
+             _dtype_code(weight), eps, T, d, _ptr(h), _ptr(xn), _ptr(smooth), a_bits, _ptr(codes), _ptr(scales),
+             stream=stream)
 
 
 def qe_colmean_abs(W, w, stream=None):

@@ -12,60 +12,12 @@
 
 #include <algorithm>
 
+#include "qe_act.h"
 #include "qe_dma.h"
 #include "qe_internal.h"
 #include "qe_splits.h"
 
 namespace qe {
-
-// ---------------------------------------------------------------- helpers
-__device__ inline float bf16_bits_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
-
-// a / b correctly rounded, given inv_b = RN(1/b).  One multiply and two fused
-// multiply-adds (Markstein's correction).  Exact for |a| in [2^-100, 2^100] and b
-// in [2^-90, 2^90] with quotients of magnitude >= 2^-3; callers fall back to the
-// IEEE division outside that domain.
-__device__ inline float div_markstein(float a, float b, float inv_b) {
-    float q0 = a * inv_b;
-    float r = __builtin_fmaf(-b, q0, a);
-    return __builtin_fmaf(r, inv_b, q0);
-}
-
-__device__ inline bool in_markstein_range(float a) {
-    float m = __builtin_fabsf(a);
-    return (m >= 0x1p-100f && m <= 0x1p100f) || m == 0.0f;
-}
-
-// x / s exactly as IEEE float32 division
-__device__ inline float smooth_div(float x, float s, float inv_s) {
-    return in_markstein_range(x) ? div_markstein(x, s, inv_s) : x / s;
-}
-
-// load 8 consecutive activations as float
-__device__ inline void load8(const void* x, int x_dtype, size_t idx, float out[8]) {
-    if (x_dtype == QE_BF16) {
-        v4u p = *reinterpret_cast<const v4u*>(reinterpret_cast<const uint16_t*>(x) + idx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            out[2 * i] = __uint_as_float(p[i] << 16);
-            out[2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
-        }
-    } else {
-        const v4f* p = reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(x) + idx);
-        v4f a = p[0], b = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            out[i] = a[i];
-            out[4 + i] = b[i];
-        }
-    }
-}
-
-__device__ inline float wave_max(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-    return v;
-}
 
 // ---------------------------------------------------------------- a1: quant
 // One workgroup per token; each thread owns up to QA_IT groups of 8 consecutive
@@ -75,36 +27,6 @@ __device__ inline float wave_max(float v) {
 // correction, with the exact division as a wave-uniform fallback outside its
 // verified domain) and round half to even.
 constexpr int QA_IT = 4;
-
-template <bool kHasInv>
-__device__ inline void smooth8(const float* __restrict__ smooth, const float* __restrict__ inv_smooth, int j,
-                               float v[8]) {
-    const v4f s0 = *reinterpret_cast<const v4f*>(smooth + j), s1 = *reinterpret_cast<const v4f*>(smooth + j + 4);
-    float s[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-    float is[8];
-    if (kHasInv) {
-        const v4f i0 = *reinterpret_cast<const v4f*>(inv_smooth + j), i1 = *reinterpret_cast<const v4f*>(inv_smooth + j + 4);
-        is[0] = i0[0]; is[1] = i0[1]; is[2] = i0[2]; is[3] = i0[3];
-        is[4] = i1[0]; is[5] = i1[1]; is[6] = i1[2]; is[7] = i1[3];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) is[i] = 1.0f / s[i];
-    }
-    bool ok = true;
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        r[i] = div_markstein(v[i], s[i], is[i]);
-        ok = ok && in_markstein_range(v[i]);
-    }
-    if (__builtin_expect(__any(!ok), 0)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!in_markstein_range(v[i])) r[i] = v[i] / s[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = r[i];
-}
 
 template <bool kHasInv>
 __global__ __launch_bounds__(1024) void quant_act_kernel(const void* __restrict__ x, int x_dtype,

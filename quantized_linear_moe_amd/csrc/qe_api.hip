@@ -13,6 +13,7 @@
 #include "qe_calib.h"
 #include "qe_lowrank.h"
 #include "qe_internal.h"
+#include "qe_mx4.h"
 
 namespace qe {
 hipError_t skinny_set_attributes();
@@ -49,13 +50,18 @@ int hip_fail(hipError_t e) {
         if (!(cond)) return (code); \
     } while (0)
 
+// microscaled 4-bit operands on both sides (the main product and its layouts are qe_mx4.h's)
+inline bool mx4(const qe_linear* lin) { return lin->a_bits == 4; }
+// per-token integer activation codes
+inline bool int_codes(const qe_linear* lin) { return lin->a_bits == 6 || lin->a_bits == 8; }
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int validate_linear(const qe_linear* lin) {
     QE_CHECK(lin != nullptr, QE_ERR_INVALID_ARG);
     QE_CHECK(lin->d_in > 0 && lin->d_out > 0, QE_ERR_INVALID_ARG);
     QE_CHECK(lin->w_bits == 3 || lin->w_bits == 4, QE_ERR_INVALID_ARG);
-    QE_CHECK(lin->a_bits == 6 || lin->a_bits == 8 || lin->a_bits == 16, QE_ERR_INVALID_ARG);
+    QE_CHECK(int_codes(lin) || mx4(lin) || lin->a_bits == 16, QE_ERR_INVALID_ARG);
     QE_CHECK(!(lin->w_bits == 3 && lin->a_bits != 16), QE_ERR_UNSUPPORTED);
     QE_CHECK(lin->r_shared >= 0 && lin->r_shared <= kMaxRank, QE_ERR_INVALID_ARG);
     QE_CHECK(lin->n_routed >= 0 && lin->n_routed <= kMaxRouted, QE_ERR_INVALID_ARG);
@@ -68,8 +74,8 @@ int validate_linear(const qe_linear* lin) {
     QE_CHECK(lin->d_out % 16 == 0, QE_ERR_UNSUPPORTED);
     QE_CHECK(lin->d_in % 128 == 0, QE_ERR_UNSUPPORTED);
     // 16 * |acc| must stay below 2^31 on the int8 path: 16 * 127 * 7 * d_in
-    QE_CHECK(lin->a_bits == 16 || (int64_t)lin->d_in * 16 * 127 * 7 < (int64_t)INT32_MAX, QE_ERR_UNSUPPORTED);
-    QE_CHECK(lin->a_bits == 16 || lin->d_in <= 32768, QE_ERR_UNSUPPORTED);  // one token row per workgroup
+    QE_CHECK(!int_codes(lin) || (int64_t)lin->d_in * 16 * 127 * 7 < (int64_t)INT32_MAX, QE_ERR_UNSUPPORTED);
+    QE_CHECK(!int_codes(lin) || lin->d_in <= 32768, QE_ERR_UNSUPPORTED);  // one token row per workgroup
     return QE_OK;
 }
 
@@ -123,7 +129,7 @@ int noalloc_scratch(void** out);
 
 // Prefill prologue in two reads of x (route pass, then expert-sorted quantization), for
 // bf16 activations; the workspace is sized for it whatever the activation type
-bool two_pass_sized(const qe_linear* lin, int T) { return lin->a_bits != 16 && T > kSkinnyMaxT; }
+bool two_pass_sized(const qe_linear* lin, int T) { return int_codes(lin) && T > kSkinnyMaxT; }
 // few-token prefill with bf16 x: the one-launch prologue where its shape limits allow
 bool row_prologue(const qe_linear* lin, int T, int x_dtype) {
     return two_pass_sized(lin, T) && x_dtype == QE_BF16 &&
@@ -151,10 +157,11 @@ PrepLayout prep_layout(const qe_linear* lin) {
     L.n_cols_pad = (L.n_cols + 15) / 16 * 16;
     size_t off = 0;
     L.w_tiled = off;
-    L.w_tiled_bytes = lin->w_bits == 4 ? d_out * d_in / 2 : d_out * d_in * 3 / 8;
+    const size_t d_out32 = (d_out + 31) / 32 * 32;  // the microscaled tiles hold whole 32-channel blocks
+    L.w_tiled_bytes = mx4(lin) ? d_out32 * d_in / 2 : lin->w_bits == 4 ? d_out * d_in / 2 : d_out * d_in * 3 / 8;
     off = align256(off + L.w_tiled_bytes);
     L.w_scale = off;
-    off = align256(off + d_out * 4);
+    off = align256(off + (mx4(lin) ? d_out32 * d_in / kMxBlock : d_out * 4));
     L.smooth = off;
     off = align256(off + (L.has_smooth ? d_in * 4 : 0));
     L.inv_smooth = off;
@@ -174,16 +181,17 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     const PrepLayout P = prep_layout(lin);
     const size_t t = T > 0 ? T : 0;
     W.xproj_ksplit = xproj_ksplit(T, lin->d_in, P.n_cols_pad);
-    W.skinny_ksplit = lin->a_bits != 16 ? 0
+    W.skinny_ksplit = mx4(lin)            ? mx4_plan(T, lin->d_in, lin->d_out).ksplit
+                      : lin->a_bits != 16 ? 0
                       : T <= kSkinnyMaxT ? skinny_ksplit(lin->d_in, lin->d_out)
                                          : gemm_a16_ksplit(T, lin->d_in, lin->d_out, lin->w_bits);
-    const bool fused_decode = T <= kSkinnyMaxT && (lin->a_bits == 16 || lin->w_bits == 4);
+    const bool fused_decode = !mx4(lin) && T <= kSkinnyMaxT && (lin->a_bits == 16 || lin->w_bits == 4);
     const DecodePlan D = fused_decode ? decode_plan(lin->d_in, lin->d_out, lin->w_bits, P.n_cols_pad, T) : DecodePlan{};
     size_t off = 0;
     W.codes = off;
-    off = align256(off + (lin->a_bits == 16 ? 0 : t * lin->d_in));
+    off = align256(off + (lin->a_bits == 16 ? 0 : mx4(lin) ? t * (lin->d_in / 2) : t * lin->d_in));
     W.s_x = off;
-    off = align256(off + t * 4);
+    off = align256(off + (mx4(lin) ? t * (lin->d_in / kMxBlock) : t * 4));
     W.part = off;
     const int xks = std::max({W.xproj_ksplit, T <= kSkinnyMaxT ? skinny_ksplit_proj(lin->d_in) : 1, D.ks_p});
     const bool two_pass = two_pass_sized(lin, T);
@@ -209,9 +217,10 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     off = align256(off + t * P.rs_pad * 2);
     W.v = off;
     off = align256(off + t * P.rr_pad * 2);
-    W.gemm_ksplit = lin->a_bits != 16 ? gemm_ksplit(T, lin->d_in, lin->d_out) : 1;
+    W.gemm_ksplit = int_codes(lin) ? gemm_ksplit(T, lin->d_in, lin->d_out) : 1;
     W.skinny = off;
-    off = align256(off + (size_t)std::max({W.skinny_ksplit, D.ks_m, W.gemm_ksplit > 1 ? W.gemm_ksplit : 0}) * t *
+    const int skinny_parts = mx4(lin) && W.skinny_ksplit == 1 ? 0 : W.skinny_ksplit;
+    off = align256(off + (size_t)std::max({skinny_parts, D.ks_m, W.gemm_ksplit > 1 ? W.gemm_ksplit : 0}) * t *
                              lin->d_out * 4);
     W.total = off;
     return W;
@@ -334,28 +343,11 @@ size_t qe_prepared_bytes(const qe_linear* lin) {
     return prep_layout(lin).total;
 }
 
-int qe_prepare(const qe_linear* lin, const void* w_packed, const float* w_scale, const float* smooth,
-               const uint16_t* A_s, const uint16_t* B_s, const uint16_t* A_r, const uint16_t* B_r, const uint16_t* R,
-               void* prep, void* stream) {
-    int st = validate_linear(lin);
-    if (st) return st;
-    QE_CHECK(w_packed && w_scale && prep, QE_ERR_INVALID_ARG);
-    QE_CHECK((lin->r_shared > 0) == (A_s != nullptr) && (lin->r_shared > 0) == (B_s != nullptr), QE_ERR_INVALID_ARG);
-    QE_CHECK((lin->n_routed > 0) == (A_r != nullptr) && (lin->n_routed > 0) == (B_r != nullptr) &&
-                 (lin->n_routed > 0) == (R != nullptr),
-             QE_ERR_INVALID_ARG);
-    QE_CHECK(!(lin->a_bits == 16 && smooth != nullptr), QE_ERR_INVALID_ARG);
-    for (const void* p : {w_packed, (const void*)w_scale, (const void*)prep})
-        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+// Smoothing factors, adapters and router into the prepared buffer (everything but the weights).
+static int prepare_rest(const qe_linear* lin, const float* smooth, const uint16_t* A_s, const uint16_t* B_s,
+                        const uint16_t* A_r, const uint16_t* B_r, const uint16_t* R, void* prep, hipStream_t s) {
     const PrepLayout L = prep_layout(lin);
-    hipStream_t s = S(stream);
     const int d_in = lin->d_in, d_out = lin->d_out;
-    if (lin->w_bits == 4) {
-        QE_TRY_HIP(launch_prep_w4(reinterpret_cast<const uint8_t*>(w_packed), d_out, d_in, at<uint8_t>(prep, L.w_tiled), s));
-    } else {
-        QE_TRY_HIP(launch_prep_w3(reinterpret_cast<const uint32_t*>(w_packed), d_out, d_in, at<uint32_t>(prep, L.w_tiled), s));
-    }
-    QE_TRY_HIP(hipMemcpyAsync(at<void>(prep, L.w_scale), w_scale, (size_t)d_out * 4, hipMemcpyDeviceToDevice, s));
     if (L.has_smooth)
         QE_TRY_HIP(launch_prep_smooth(smooth, d_in, at<float>(prep, L.smooth), at<float>(prep, L.inv_smooth), s));
     // Mt: [A_s^T ; R^T ; A_1^T .. A_N^T], zero rows in the padding
@@ -375,6 +367,53 @@ int qe_prepare(const qe_linear* lin, const void* w_packed, const float* w_scale,
                                          at<uint16_t>(prep, L.bt_r) + (size_t)e * d_out * L.rr_pad, L.rr_pad, d_out, s));
     }
     return QE_OK;
+}
+
+int qe_prepare(const qe_linear* lin, const void* w_packed, const float* w_scale, const float* smooth,
+               const uint16_t* A_s, const uint16_t* B_s, const uint16_t* A_r, const uint16_t* B_r, const uint16_t* R,
+               void* prep, void* stream) {
+    int st = validate_linear(lin);
+    if (st) return st;
+    QE_CHECK(!mx4(lin), QE_ERR_UNSUPPORTED);  // microscaled weights: qe_mx4_prepare
+    QE_CHECK(w_packed && w_scale && prep, QE_ERR_INVALID_ARG);
+    QE_CHECK((lin->r_shared > 0) == (A_s != nullptr) && (lin->r_shared > 0) == (B_s != nullptr), QE_ERR_INVALID_ARG);
+    QE_CHECK((lin->n_routed > 0) == (A_r != nullptr) && (lin->n_routed > 0) == (B_r != nullptr) &&
+                 (lin->n_routed > 0) == (R != nullptr),
+             QE_ERR_INVALID_ARG);
+    QE_CHECK(!(lin->a_bits == 16 && smooth != nullptr), QE_ERR_INVALID_ARG);
+    for (const void* p : {w_packed, (const void*)w_scale, (const void*)prep})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    const PrepLayout L = prep_layout(lin);
+    hipStream_t s = S(stream);
+    const int d_in = lin->d_in, d_out = lin->d_out;
+    if (lin->w_bits == 4) {
+        QE_TRY_HIP(launch_prep_w4(reinterpret_cast<const uint8_t*>(w_packed), d_out, d_in, at<uint8_t>(prep, L.w_tiled), s));
+    } else {
+        QE_TRY_HIP(launch_prep_w3(reinterpret_cast<const uint32_t*>(w_packed), d_out, d_in, at<uint32_t>(prep, L.w_tiled), s));
+    }
+    QE_TRY_HIP(hipMemcpyAsync(at<void>(prep, L.w_scale), w_scale, (size_t)d_out * 4, hipMemcpyDeviceToDevice, s));
+    return prepare_rest(lin, smooth, A_s, B_s, A_r, B_r, R, prep, s);
+}
+
+int qe_mx4_prepare(const qe_linear* lin, const uint8_t* w_codes, const uint8_t* w_scales, const float* smooth,
+                   const uint16_t* A_s, const uint16_t* B_s, const uint16_t* A_r, const uint16_t* B_r,
+                   const uint16_t* R, void* prep, void* stream) {
+    int st = validate_linear(lin);
+    if (st) return st;
+    QE_CHECK(mx4(lin), QE_ERR_INVALID_ARG);
+    QE_CHECK(w_codes && w_scales && prep, QE_ERR_INVALID_ARG);
+    QE_CHECK((lin->r_shared > 0) == (A_s != nullptr) && (lin->r_shared > 0) == (B_s != nullptr), QE_ERR_INVALID_ARG);
+    QE_CHECK((lin->n_routed > 0) == (A_r != nullptr) && (lin->n_routed > 0) == (B_r != nullptr) &&
+                 (lin->n_routed > 0) == (R != nullptr),
+             QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)w_codes, (const void*)w_scales, (const void*)prep, (const void*)smooth,
+                          (const void*)A_s, (const void*)B_s, (const void*)A_r, (const void*)B_r, (const void*)R})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    const PrepLayout L = prep_layout(lin);
+    hipStream_t s = S(stream);
+    QE_TRY_HIP(launch_mx4_prep(w_codes, w_scales, lin->d_out, lin->d_in, at<uint8_t>(prep, L.w_tiled),
+                               at<uint32_t>(prep, L.w_scale), s));
+    return prepare_rest(lin, smooth, A_s, B_s, A_r, B_r, R, prep, s);
 }
 
 size_t qe_workspace_bytes(const qe_linear* lin, int32_t T) {
@@ -515,6 +554,7 @@ int qe_wq_gemm(const qe_linear* lin, const int8_t* codes, const float* s_x, cons
                int32_t* acc_debug, void* ws, size_t ws_bytes, void* stream) {
     int st = validate_forward_common(lin, T, x_dtype, x, ws, ws_bytes);
     if (st) return st;
+    QE_CHECK(!mx4(lin), QE_ERR_UNSUPPORTED);  // qe_mx4_gemm
     if (T == 0) return QE_OK;
     QE_CHECK(y != nullptr, QE_ERR_INVALID_ARG);
     QE_CHECK(aligned16(y), QE_ERR_ALIGNMENT);
@@ -527,6 +567,106 @@ int qe_wq_gemm(const qe_linear* lin, const int8_t* codes, const float* s_x, cons
     QE_CHECK((v == nullptr) == (expert == nullptr), QE_ERR_INVALID_ARG);
     return run_gemm(lin, codes, s_x, x, x_dtype, T, u, v, expert, lin->a_bits == 16 ? nullptr : perm, y, acc_debug, ws,
                     S(stream));
+}
+
+// ------------------------------------------------------------------ microscaled 4-bit
+int qe_mx4_quant(const void* x, int32_t x_dtype, const float* smooth, int32_t multiply, int32_t T, int32_t d,
+                 uint8_t* codes, uint8_t* scales, void* stream) {
+    QE_CHECK(T >= 0 && d > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(x_dtype == QE_F32 || x_dtype == QE_BF16, QE_ERR_INVALID_ARG);
+    QE_CHECK(multiply == 0 || multiply == 1, QE_ERR_INVALID_ARG);
+    QE_CHECK(d % kMxBlock == 0, QE_ERR_UNSUPPORTED);
+    if (T == 0) return QE_OK;
+    QE_CHECK(x && codes && scales, QE_ERR_INVALID_ARG);
+    for (const void* p : {x, (const void*)smooth, (const void*)codes, (const void*)scales})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_TRY_HIP(launch_mx4_quant(x, x_dtype, smooth, multiply != 0, T, d, codes, scales, S(stream)));
+    return QE_OK;
+}
+
+int qe_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int32_t T, int32_t d, void* x, int32_t x_dtype,
+                   void* stream) {
+    QE_CHECK(T >= 0 && d > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(x_dtype == QE_F32 || x_dtype == QE_BF16, QE_ERR_INVALID_ARG);
+    QE_CHECK(d % kMxBlock == 0, QE_ERR_UNSUPPORTED);
+    if (T == 0) return QE_OK;
+    QE_CHECK(x && codes && scales, QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)x, (const void*)codes, (const void*)scales})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_TRY_HIP(launch_mx4_dequant(codes, scales, T, d, x, x_dtype, S(stream)));
+    return QE_OK;
+}
+
+static int run_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_t* scales, int T, const uint16_t* u,
+                        const uint16_t* v, const int32_t* expert, const int32_t* perm, float* y, void* ws,
+                        hipStream_t s) {
+    const PrepLayout P = prep_layout(lin);
+    const Mx4Plan plan = mx4_plan(T, lin->d_in, lin->d_out);
+    Mx4Gemm G{};
+    G.codes = codes;
+    G.scales = scales;
+    G.w_tiled = at<const uint8_t>(lin->prep, P.w_tiled);
+    G.w_scale = at<const uint32_t>(lin->prep, P.w_scale);
+    if (P.rs_pad > 0 && u) {
+        G.u = u;
+        G.bt_s = at<const uint16_t>(lin->prep, P.bt_s);
+        G.rs_pad = P.rs_pad;
+    }
+    if (P.rr_pad > 0 && v) {
+        G.v = v;
+        G.expert = expert;
+        G.bt_r = at<const uint16_t>(lin->prep, P.bt_r);
+        G.rr_pad = P.rr_pad;
+        G.n_r = lin->n_routed;
+    }
+    G.perm = perm;
+    G.y = y;
+    G.part = plan.ksplit > 1 ? at<float>(ws, ws_layout(lin, T).skinny) : nullptr;
+    G.T = T;
+    G.d_in = lin->d_in;
+    G.d_out = lin->d_out;
+    G.y_bf16 = lin->y_dtype == QE_BF16;
+    QE_TRY_HIP(launch_mx4_gemm(G, plan, s));
+    return QE_OK;
+}
+
+int qe_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_t* scales, int32_t T, const uint16_t* u,
+                const uint16_t* v, const int32_t* expert, const int32_t* perm, float* y, void* ws, size_t ws_bytes,
+                void* stream) {
+    int st = validate_forward_common(lin, T, QE_BF16, nullptr, ws, ws_bytes);
+    if (st) return st;
+    QE_CHECK(mx4(lin), QE_ERR_INVALID_ARG);
+    QE_CHECK((v == nullptr) == (expert == nullptr), QE_ERR_INVALID_ARG);
+    QE_CHECK((!u || lin->r_shared > 0) && (!v || lin->n_routed > 0), QE_ERR_INVALID_ARG);
+    if (T == 0) return QE_OK;
+    QE_CHECK(codes && scales && y, QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)codes, (const void*)scales, (const void*)u, (const void*)v, (const void*)expert,
+                          (const void*)perm, (const void*)y})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    return run_mx4_gemm(lin, codes, scales, T, u, v, expert, perm, y, ws, S(stream));
+}
+
+// ------------------------------------------------------------------ residual addition + norm
+int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* weight, int32_t weight_dtype,
+                   float eps, int32_t T, int32_t d, void* h, void* xn, const float* smooth, int32_t a_bits, void* codes,
+                   void* scales, void* stream) {
+    QE_CHECK(T >= 0 && d > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(x_dtype == QE_F32 || x_dtype == QE_BF16, QE_ERR_INVALID_ARG);
+    QE_CHECK(weight_dtype == QE_F32 || weight_dtype == QE_BF16, QE_ERR_INVALID_ARG);
+    QE_CHECK(eps > 0.0f && eps <= 3.402823466e38f, QE_ERR_INVALID_ARG);  // also rejects NaN
+    QE_CHECK(a_bits == 0 || a_bits == 4 || a_bits == 6 || a_bits == 8, QE_ERR_INVALID_ARG);
+    QE_CHECK(d % (a_bits == 4 ? kMxBlock : 8) == 0 && d <= 32768, QE_ERR_UNSUPPORTED);
+    if (T == 0) return QE_OK;
+    QE_CHECK(x && weight, QE_ERR_INVALID_ARG);
+    QE_CHECK(a_bits == 0 ? (!smooth && !codes && !scales) : (codes && scales), QE_ERR_INVALID_ARG);
+    QE_CHECK(h || xn || codes, QE_ERR_INVALID_ARG);
+    QE_CHECK(!h || h != xn, QE_ERR_INVALID_ARG);
+    for (const void* p : {x, res, weight, (const void*)h, (const void*)xn, (const void*)smooth, (const void*)codes,
+                          (const void*)scales})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_TRY_HIP(launch_add_rmsnorm(x, res, x_dtype, weight, weight_dtype, eps, T, d, h, xn, smooth, a_bits,
+                                  static_cast<uint8_t*>(codes), scales, S(stream)));
+    return QE_OK;
 }
 
 // ------------------------------------------------------------------ a6 unfused
@@ -619,6 +759,7 @@ int qe_linear_prologue(const qe_linear* lin, const void* x, int32_t x_dtype, int
                        void* stream) {
     int st = validate_forward_common(lin, T, x_dtype, x, ws, ws_bytes);
     if (st) return st;
+    QE_CHECK(!mx4(lin), QE_ERR_UNSUPPORTED);  // its codes are not per-token integers
     if (T == 0) return QE_OK;
     QE_CHECK(x != nullptr, QE_ERR_INVALID_ARG);
     QE_CHECK(lin->a_bits == 16 ? (codes == nullptr && s_x == nullptr) : (codes && s_x), QE_ERR_INVALID_ARG);
@@ -643,6 +784,20 @@ int qe_linear_forward(const qe_linear* lin, const void* x, int32_t x_dtype, int3
     int32_t* expert = route ? (expert_out ? expert_out : at<int32_t>(ws, W.expert)) : nullptr;
     uint16_t* u = P.rs_pad > 0 ? at<uint16_t>(ws, W.u) : nullptr;
     uint16_t* v = route ? at<uint16_t>(ws, W.v) : nullptr;
+    if (mx4(lin)) {
+        // the adapters' and the router's pass over x, the block quantization, then one product with
+        // both corrections; tiles of many tokens walk them in expert order
+        st = run_xpass(lin, x, x_dtype, T, u != nullptr, route, route, nullptr, nullptr, expert, u, v, ws, s);
+        if (st) return st;
+        int32_t* perm = route && mx4_plan(T, lin->d_in, lin->d_out).kind != 0 ? at<int32_t>(ws, W.perm) : nullptr;
+        if (perm)
+            QE_TRY_HIP(launch_bucket(expert, T, lin->n_routed, at<int32_t>(ws, W.counts), at<int32_t>(ws, W.offsets),
+                                     perm, s));
+        QE_TRY_HIP(launch_mx4_quant(x, x_dtype, at<const float>(lin->prep, P.smooth), false, T, lin->d_in,
+                                    at<uint8_t>(ws, W.codes), at<uint8_t>(ws, W.s_x), s));
+        return run_mx4_gemm(lin, at<const uint8_t>(ws, W.codes), at<const uint8_t>(ws, W.s_x), T, u, v, expert, perm,
+                            y, ws, s);
+    }
     if (T <= kSkinnyMaxT && (lin->a_bits == 16 || lin->w_bits == 4)) {
         // decode: one launch streams the projection matrix and the packed weights, one finishes;
         // with quantized activations the codes are made first and the weights meet them on the
@@ -808,7 +963,7 @@ static bool try_group_gemm(const qe_linear* const* lins, int n, int T, int8_t* c
     G.T = T;
     for (int i = 0; i < n; ++i) {
         const qe_linear* lin = lins[i];
-        if (lin->a_bits == 16 || lin->y_dtype != QE_F32) return false;
+        if (!int_codes(lin) || lin->y_dtype != QE_F32) return false;
         const PrepLayout P = prep_layout(lin);
         const WsLayout W = ws_layout(lin, T);
         if (W.gemm_ksplit > 1 || P.rs_pad > 32 || P.rr_pad > 32) return false;
@@ -846,6 +1001,7 @@ int qe_group_gemm(const qe_linear* const* lins, int32_t n_lin, const int8_t* con
         QE_CHECK(lins[i] && lins[i]->a_bits != 16, QE_ERR_INVALID_ARG);
         int st = validate_forward_common(lins[i], T, QE_BF16, nullptr, ws[i], ws_bytes[i]);
         if (st) return st;
+        QE_CHECK(!mx4(lins[i]), QE_ERR_UNSUPPORTED);
         if (T == 0) continue;
         QE_CHECK(codes[i] && s_x[i] && y[i], QE_ERR_INVALID_ARG);
         QE_CHECK(aligned16(codes[i]) && aligned16(y[i]), QE_ERR_ALIGNMENT);
@@ -873,6 +1029,7 @@ int qe_group_prologue(const qe_linear* const* lins, int32_t n_lin, const void* x
     int st = validate_group(lins, n_lin, T, x_dtype, x, ws, ws_bytes);
     if (st) return st;
     QE_CHECK(codes && s_x && u && v && expert && perm, QE_ERR_INVALID_ARG);
+    for (int i = 0; i < n_lin; ++i) QE_CHECK(!mx4(lins[i]), QE_ERR_UNSUPPORTED);
     if (T == 0) return QE_OK;
     QE_CHECK(x != nullptr, QE_ERR_INVALID_ARG);
     for (int i = 0; i < n_lin; ++i) {
@@ -1065,7 +1222,7 @@ int qe_linear_forward_top2(const qe_linear* lin, const void* x, int32_t x_dtype,
     const PrepLayout P = prep_layout(lin);
     const WsLayout W = ws_layout(lin, T);
     hipStream_t s = S(stream);
-    if (lin->a_bits != 16 && lin->w_bits == 4 && T > kSkinnyMaxT &&
+    if (int_codes(lin) && lin->w_bits == 4 && T > kSkinnyMaxT &&
         gemm_w4_top2_ok(T, lin->d_out, P.rs_pad, P.rr_pad, W.gemm_ksplit, lin->y_dtype == QE_BF16)) {
         // Both routed corrections in the main product's epilogue: the prologue also gives each
         // token's second expert (from the same router scores), one more pass of x onto the routed
@@ -1342,7 +1499,8 @@ int qe_linear_cost(const qe_linear* lin, int32_t T, int32_t n_distinct, int32_t 
     if (adapter_macs) *adapter_macs = t * (di + dout) * (rs + rr) + t * di * nr;
     if (alg_bytes) {
         double b = t * di * xb;                              // x read once
-        b += di * dout * lin->w_bits / 8.0 + dout * 4.0;     // packed weights + scales
+        b += di * dout * lin->w_bits / 8.0;                  // packed weights + scales
+        b += mx4(lin) ? di * dout / kMxBlock : dout * 4.0;
         if (lin->a_bits != 16) b += di * 4.0;                // smoothing vector
         b += t * dout * (lin->y_dtype == QE_BF16 ? 2.0 : 4.0);  // y written once
         b += (di + dout) * rs * 2.0;                         // shared expert

@@ -1,0 +1,104 @@
+// Microscaled 4-bit floating point (blocks of 32 along a row): the block format's device helpers and
+// the launch wrappers of its kernels (k_mx4.hip, k_gemm_mx4.hip) and of the fused norm (k_norm.hip).
+#pragma once
+
+#include "qe_internal.h"
+
+namespace qe {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kMxBlock = 32;       // elements that share a scale
+constexpr int kMxMaxTStream = 64;  // token counts served by the weight-streaming product
+
+// float32 -> bf16 bits, round to nearest even, NaN kept
+__device__ inline uint32_t mx4_bf16_bits(float f) {
+    const __bf16 b = (__bf16)f;
+    return (uint32_t)__builtin_bit_cast(uint16_t, b);
+}
+
+// largest of a 32-bit unsigned value over the 4 lanes 4q..4q+3 (all active)
+__device__ inline uint32_t quad_umax(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // lanes 1,0,3,2
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // lanes 2,3,0,1
+}
+
+// The block form of 8 channels j..j+7 of one row, the other 24 of the block in the neighbouring
+// lanes of the quad (lane 4q + i holds the block's channels 8i..8i+7): with E = floor(log2 amax)
+// the block's scale is 2^(E - 2) (byte E - 2 + 127, at least 0), and the codes are the values
+// over it rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to the even code), at most 6.
+// amax is compared as bits, so a NaN or an infinity is the largest: such a block gets scale byte
+// 255 (NaN) and zero codes.
+__device__ inline uint32_t mx4_codes8(const float v[8], uint32_t* scale_byte) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const uint32_t field = quad_umax(m) >> 23;
+    const uint32_t sc = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
+    *scale_byte = sc;
+    uint32_t c = 0;
+    if (__builtin_expect(__any(sc == 0u), 0)) {
+        // scale 2^-127 is not a normal float32: twice the values over 2^-126 (exact, all below 2^-123)
+        const float f = sc == 0u ? 2.0f : 1.0f, s = __uint_as_float(max(sc, 1u) << 23);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * f, v[1] * f, s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * f, v[3] * f, s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * f, v[5] * f, s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * f, v[7] * f, s, 3);
+    } else {
+        const float s = __uint_as_float(sc << 23);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+    }
+    return sc == 255u ? 0u : c;
+}
+
+// mx4_codes8 into a row's codes and scales
+__device__ inline void mx4_store8(const float v[8], uint8_t* codes_row, uint8_t* scales_row, int j) {
+    uint32_t sc;
+    const uint32_t c = mx4_codes8(v, &sc);
+    *reinterpret_cast<uint32_t*>(codes_row + j / 2) = c;
+    if ((j & 31) == 0) scales_row[j >> 5] = (uint8_t)sc;
+}
+
+// ------------------------------------------------------------------ launch wrappers
+hipError_t launch_add_rmsnorm(const void* x, const void* res, int x_dtype, const void* w, int w_dtype, float eps,
+                              int T, int d, void* h, void* xn, const float* smooth, int a_bits, uint8_t* codes,
+                              void* scales, hipStream_t st);
+hipError_t launch_mx4_quant(const void* x, int x_dtype, const float* smooth, bool multiply, int T, int d,
+                            uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T, int d, void* x, int x_dtype,
+                              hipStream_t st);
+// canonical codes and scales of [d_out][d_in] weights into the product's tiles (see k_mx4.hip)
+hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, int d_out, int d_in, uint8_t* w_tiled,
+                           uint32_t* w_scale, hipStream_t st);
+
+// How the product runs for T tokens: which kernel and how many K splits (more than one: float32
+// partials [ksplit][T][d_out] in the workspace, added by a finish kernel)
+struct Mx4Plan {
+    int kind;    // 0: weight streaming (T <= kMxMaxTStream); else the tile's tokens (and channels)
+    int ksplit;
+};
+Mx4Plan mx4_plan(int T, int d_in, int d_out);
+
+struct Mx4Gemm {
+    const uint8_t* codes;      // [T][d_in/2]
+    const uint8_t* scales;     // [T][d_in/32]
+    const uint8_t* w_tiled;
+    const uint32_t* w_scale;
+    const uint16_t* u;         // [T][rs_pad] or NULL
+    const uint16_t* bt_s;      // [d_out][rs_pad]
+    const uint16_t* v;         // [T][rr_pad] or NULL
+    const int32_t* expert;     // [T]
+    const uint16_t* bt_r;      // [n_r][d_out][rr_pad]
+    const int32_t* perm;       // [T] or NULL
+    float* y;                  // [T][d_out] (bf16 elements when y_bf16)
+    float* part;               // [ksplit][T][d_out] when ksplit > 1
+    int T, d_in, d_out, rs_pad, rr_pad, n_r;
+    bool y_bf16;
+};
+hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st);
+
+}  // namespace qe

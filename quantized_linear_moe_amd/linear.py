@@ -38,10 +38,14 @@ class QELinear:
     @classmethod
     def from_params(cls, params: Dict[str, object], w_bits: int, a_bits: int, device="cuda",
                     packed: Optional[np.ndarray] = None, w_scale: Optional[np.ndarray] = None) -> "QELinear":
-        """params: W_f (float32 [d_out, d_in]) or (packed, w_scale); s; A_s, B_s, A_r, B_r, R (bf16)."""
+        """params: W_f (float32 [d_out, d_in]) or (packed, w_scale; with a_bits 4
+        qe_mx4_quant's codes and scales); s; A_s, B_s, A_r, B_r, R (bf16)."""
         A_s, B_s, A_r, B_r, R = (params.get(k) for k in ("A_s", "B_s", "A_r", "B_r", "R"))
         s = params.get("s") if a_bits != 16 else None  # weight-only layers carry no smoothing
-        if packed is None:
+        if packed is None and a_bits == 4:  # microscaled weights are quantized on the device
+            W_f = params["W_f"]
+            d_out, d_in = W_f.shape
+        elif packed is None:
             W_f = params["W_f"]
             d_out, d_in = W_f.shape
             packed, w_scale = L.qe_pack_weights(W_f, s, w_bits)
@@ -58,6 +62,17 @@ class QELinear:
             A_r=_dev(A_r, dev, torch.bfloat16) if n_r else None, B_r=_dev(B_r, dev, torch.bfloat16) if n_r else None,
             R=_dev(R, dev, torch.bfloat16) if n_r else None,
         )
+        if a_bits == 4:
+            if packed is None:
+                bufs["w_packed"] = torch.empty(d_out, d_in // 2, dtype=torch.uint8, device=dev)
+                bufs["w_scale"] = torch.empty(d_out, d_in // 32, dtype=torch.uint8, device=dev)
+                L.qe_mx4_quant(_dev(W_f, dev, torch.float32), bufs["smooth"], bufs["w_packed"], bufs["w_scale"],
+                               multiply=True)
+            L.qe_mx4_prepare(self.lin, bufs["w_packed"], bufs["w_scale"], bufs["smooth"], bufs["A_s"], bufs["B_s"],
+                             bufs["A_r"], bufs["B_r"], bufs["R"], self.prep)
+            torch.cuda.current_stream(dev).synchronize()
+            self.packed, self.w_scale = bufs["w_packed"], bufs["w_scale"]
+            return self
         L.qe_prepare(self.lin, bufs["w_packed"], bufs["w_scale"], bufs["smooth"], bufs["A_s"], bufs["B_s"],
                      bufs["A_r"], bufs["B_r"], bufs["R"], self.prep)
         torch.cuda.current_stream(dev).synchronize()  # inputs may be freed after the prepare work
