@@ -13,6 +13,7 @@
 // streaming for up to 64 tokens (bound by the reads of the weights).
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qe_dma.h"
 #include "qe_internal.h"
@@ -41,29 +42,36 @@ __device__ inline void store_out(float* y, size_t idx, float v, bool y_bf16) {
     else y[idx] = v;
 }
 
-constexpr int TS_NS = 4;  // K steps in the LDS ring of the tile kernel
-
 }  // namespace
 
 // ------------------------------------------------------------------ tiles
-// BM tokens x BN channels per workgroup of 4 waves (2 x 2), 128 channels of K per step.  Code rows and
-// weight tiles go global -> LDS by DMA through a ring of TS_NS steps, TS_NS - 1 ahead.  Each wave
-// holds BM/64 x BN/64 blocks of 32 x 32.  The fragments of the next half step are requested before the MFMAs
-// of the current one, and the barrier that frees a ring slot stands between the two halves of a step,
-// with the second half's fragments already in registers: the matrix cores meet it with work queued.
-// Code rows of a step are 64 bytes, four 16-byte chunks stored at chunk ^ ((row >> 1) & 3) so that 8
-// consecutive rows reach all banks.
-template <int BM, int BN>
-__global__ __launch_bounds__(256, 1) void gemm_mx4_kernel(Mx4Gemm G, int n_tm, int ksplit) {
-    constexpr int MB = BM / 64, NB = BN / 64;              // 32x32 blocks per wave
+// BM tokens x BN channels per workgroup of WM x WN waves, 128 channels of K per step.  Codes and scales
+// go global -> LDS by DMA through a ring of NS steps, NS - 1 ahead; each wave holds MB x NB blocks of
+// 32 x 32.  The fragments of a half step are read while the MFMAs of the one before run, and the barrier
+// that frees a ring slot stands between the two halves of a step, when the second half's fragments are
+// already in registers: the matrix cores meet it with work at hand.
+//
+// Adapter terms are more steps of the same ring: 32 ranks of u (or v) and of B_s (or of one expert's
+// B_e) have the bytes of 128 codes and the same fragments, 16 ranks per half, multiplied in bf16.  A
+// routed step is masked to its expert's rows; only experts that some row of the tile uses are met.
+//
+// TA: the activations come as tiles like the weights (mx4_prep_kernel, in the order of perm): every
+// copy is contiguous.  Otherwise from their rows: the code rows of a step are 64 bytes, four chunks of 16
+// stored at chunk ^ ((row >> 1) & 3), so that neighbouring rows lie in different banks.
+template <int BM, int BN, int WM, int WN, bool TA, int NS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, int n_tm, int n_off, int ksplit) {
+    constexpr int NW = WM * WN;
+    constexpr int MB = BM / 32 / WM, NB = BN / 32 / WN;    // 32x32 blocks per wave
     constexpr int A_ST = BM * 64, B_ST = BN * 64;          // codes per step
     constexpr int STAGE = A_ST + B_ST + BM * 4 + BN * 4;   // + scales
-    constexpr int AD = BM / 64, BD = BN / 64;              // 1 KB copies per wave
-    constexpr int SQ = BM / 64 + BN / 64, SD = (SQ + 3) / 4;  // 256-byte scale copies: in all, per wave
+    constexpr int AD = BM / 16 / NW, BD = BN / 16 / NW;    // 1 KB copies per wave
+    constexpr int SQ = BM / 64 + BN / 64, SD = (SQ + NW - 1) / NW;  // 256-byte scale copies: in all, per wave
     constexpr int OPS = AD + BD + SD;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[TS_NS * STAGE];
-    __shared__ int s_tok[BM];
-    __shared__ int s_ex[BM];
+    static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "whole copies per wave");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE];
+    __shared__ int s_tok[BM];  // the token of every row (its position in tiled form is the row's own)
+    __shared__ int s_ex[BM];   // its routed expert, -1 past the last token
+    __shared__ uint32_t s_present;
 
     // tile order: see gemm_w4_tile (each XCD walks a contiguous range of groups of 8 token tiles)
     int tm, tn;
@@ -77,198 +85,274 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_kernel(Mx4Gemm G, int n_tm, i
         tm = first + r % gs;
         tn = r / gs;
     }
-    const int m0 = tm * BM, n0 = tn * BN;
-    const int tid = threadIdx.x, wid = tid >> 6, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-    const int wm = wid & 1, wn = wid >> 1;
-    const int T = G.T, KB = G.d_in / 128, NBT = (G.d_out + 31) / 32;
+    const int m0 = tm * BM, n0 = n_off + tn * BN;
+    const int tid = threadIdx.x, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+    const int wm = wid % WM, wn = wid / WM;
+    const int T = G.T, KB = G.d_in / 128, NBT = (G.d_out + 31) / 32, NBA = (T + 31) / 32;
     const int ky = blockIdx.y;
     const int kb0 = (int)((long)ky * KB / ksplit), nk = (int)((long)(ky + 1) * KB / ksplit) - kb0;
+    const bool routed = G.v != nullptr && ky == 0;  // the first K split has the adapter terms
 
-    const bool routed = G.v != nullptr;
-    for (int r = tid; r < BM; r += 256) {
-        const int pos = min(m0 + r, T - 1);
-        const int tk = G.perm ? G.perm[pos] : pos;
-        s_tok[r] = tk;
-        s_ex[r] = (routed && m0 + r < T) ? min(max(G.expert[tk], 0), G.n_r - 1) : -1;
-    }
-    __syncthreads();
+    // The tile's tokens and routed experts.  Copies from tiles do not wait for them, so there they are
+    // loaded behind the first copies.
+    auto load_tokens = [&]() {
+        if (tid == 0) s_present = 0;
+        __syncthreads();
+        for (int r = tid; r < BM; r += 64 * NW) {
+            const int pos = min(m0 + r, T - 1);
+            const int tk = G.perm ? G.perm[pos] : pos;
+            const int e = (routed && m0 + r < T) ? min(max(G.expert[tk], 0), G.n_r - 1) : -1;
+            s_tok[r] = tk;
+            s_ex[r] = e;
+            if (e >= 0) atomicOr(&s_present, 1u << e);
+        }
+        __syncthreads();
+    };
+    if constexpr (!TA) load_tokens();
 
     const uint32_t lds0 = lds_addr(smem);
-    // copy sources; A copy q covers rows 16q..16q+15: lane i fetches the chunk stored at slot i%4
-    const uint8_t* a_src[AD];
+    const uint8_t *a_src[AD], *b_src[BD], *s_src[SD];
 #pragma unroll
     for (int p = 0; p < AD; ++p) {
-        const int r = 16 * (wid + 4 * p) + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
-        a_src[p] = G.codes + (size_t)s_tok[r] * (G.d_in / 2) + (size_t)kb0 * 64 + c * 16;
+        const int q = wid + NW * p;
+        if constexpr (TA) {  // as for B below
+            const int mb = min(m0 / 32 + (q >> 1), NBA - 1);
+            a_src[p] = G.codes + (((size_t)mb * KB + kb0) * 2 + (q & 1)) * 1024 + lane * 16;
+        } else {  // rows 16q..16q+15: lane i fetches the chunk stored at slot i%4
+            const int r = 16 * q + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
+            a_src[p] = G.codes + (size_t)s_tok[r] * (G.d_in / 2) + (size_t)kb0 * 64 + c * 16;
+        }
     }
-    const uint8_t* b_src[BD];  // B copy q: half step q & 1 of channel block q >> 1
 #pragma unroll
-    for (int p = 0; p < BD; ++p) {
-        const int q = wid + 4 * p, nb = min(n0 / 32 + (q >> 1), NBT - 1);
+    for (int p = 0; p < BD; ++p) {  // B copy q: half step q & 1 of channel block q >> 1
+        const int q = wid + NW * p, nb = min(n0 / 32 + (q >> 1), NBT - 1);
         b_src[p] = G.w_tiled + (((size_t)nb * KB + kb0) * 2 + (q & 1)) * 1024 + lane * 16;
     }
-    const uint8_t* s_src[SD];  // scale copies: 64 rows of A each, then 64 channels of B each
-    int s_dst[SD], s_step[SD];
+    int s_step[SD];  // scale copies: 64 rows of A each, then 64 channels of B each
 #pragma unroll
     for (int p = 0; p < SD; ++p) {
-        const int q = (wid + 4 * p) % SQ;  // fewer copies than waves: repeated, the same bytes
-        if (q < BM / 64) {
-            s_src[p] = G.scales + (size_t)s_tok[q * 64 + lane] * (G.d_in / 32) + (size_t)kb0 * 4;
-            s_step[p] = 4;
-        } else {
+        const int q = (wid + NW * p) % SQ;  // fewer copies than waves: repeated, the same bytes
+        s_step[p] = 128;
+        if (q >= BM / 64) {
             const int nb = min(n0 / 32 + (q - BM / 64) * 2 + lh, NBT - 1);
             s_src[p] = reinterpret_cast<const uint8_t*>(G.w_scale + ((size_t)nb * KB + kb0) * 32 + lr);
-            s_step[p] = 128;
+        } else if (TA) {
+            const int mb = min(m0 / 32 + q * 2 + lh, NBA - 1);
+            s_src[p] = G.scales + ((size_t)mb * KB + kb0) * 128 + lr * 4;
+        } else {
+            s_src[p] = G.scales + (size_t)s_tok[q * 64 + lane] * (G.d_in / 32) + (size_t)kb0 * 4;
+            s_step[p] = 4;
         }
-        s_dst[p] = A_ST + B_ST + q * 256;
     }
-    auto issue = [&](int slot, int i) {
-        const uint32_t base = lds0 + slot * STAGE;
-#pragma unroll
-        for (int p = 0; p < AD; ++p) dma16(a_src[p] + (size_t)i * 64, base + (wid + 4 * p) * 1024);
-#pragma unroll
-        for (int p = 0; p < BD; ++p) dma16(b_src[p] + (size_t)i * 2048, base + A_ST + (wid + 4 * p) * 1024);
-#pragma unroll
-        for (int p = 0; p < SD; ++p) dma4(s_src[p] + (size_t)i * s_step[p], base + s_dst[p]);
-    };
-    struct Frag {
-        v4i a[MB], b[NB];
-    };
-    struct Scale {
-        uint32_t a[MB], b[NB];
-    };
-    auto read = [&](Frag& f, int slot, int h) {
-        const uint8_t* st = smem + slot * STAGE;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const int row = (wm * MB + m) * 32 + lr;
-            f.a[m] = *reinterpret_cast<const v4i*>(st + row * 64 + (((h * 2 + lh) ^ ((row >> 1) & 3)) << 4));
+    // copy c of a step of codes into the ring slot at LDS address `base`; its source moves on (more != 0)
+    auto issue = [&](int c, uint32_t base, int more) {
+        if (c < AD) {
+            dma16(a_src[c], base + (wid + NW * c) * 1024);
+            a_src[c] += more * (TA ? 2048 : 64);
+        } else if (c < AD + BD) {
+            const int p = c - AD;
+            dma16(b_src[p], base + A_ST + (wid + NW * p) * 1024);
+            b_src[p] += more * 2048;
+        } else {
+            const int p = c - AD - BD;
+            dma4(s_src[p], base + A_ST + B_ST + (wid + NW * p) % SQ * 256);
+            s_src[p] += more * s_step[p];
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-            f.b[n] = *reinterpret_cast<const v4i*>(st + A_ST + ((wn * NB + n) * 2 + h) * 1024 + lane * 16);
     };
-    auto read_scales = [&](Scale& s, int slot) {
-        const uint8_t* st = smem + slot * STAGE + A_ST + B_ST;
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-            s.a[m] = *reinterpret_cast<const uint32_t*>(st + ((wm * MB + m) * 32 + lr) * 4) >> (8 * lh);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-            s.b[n] = *reinterpret_cast<const uint32_t*>(st + BM * 4 + ((wn * NB + n) * 32 + lr) * 4) >> (8 * lh);
+    // fragments and scales of the slot at offset `st`, numbered so that their reads can be spread between
+    // MFMAs: MB of A, then NB of B.  off: the A fragments' place (adapter steps are always in tile order)
+    v4i fa[2][MB], fb[2][NB];
+    uint32_t ra[MB], rb[NB], sa[MB], sb[NB];  // scale dwords as read, and with the lane's blocks in bytes 0 and 2
+    const int tile_a = wm * MB * 2048 + lane * 16, off_b = A_ST + wn * NB * 2048 + lane * 16;
+    const int row_a = (wm * MB * 32 + lr) * 64, row_swz = (lr >> 1) & 3;
+    const int code_a[2] = {TA ? tile_a : row_a + ((lh ^ row_swz) << 4), TA ? tile_a + 1024 : row_a + (((2 + lh) ^ row_swz) << 4)};
+    const int off_sa = A_ST + B_ST + (wm * MB * 32 + lr) * 4, off_sb = A_ST + B_ST + BM * 4 + (wn * NB * 32 + lr) * 4;
+    auto read = [&](int q, int st, int h, int off) {
+        if (q < MB) fa[h][q] = *reinterpret_cast<const v4i*>(smem + st + off + q * 2048);
+        else if (q < MB + NB)
+            fb[h][q - MB] = *reinterpret_cast<const v4i*>(smem + st + off_b + (q - MB) * 2048 + h * 1024);
     };
-
+    auto read_scale = [&](int q, int st) {
+        if (q < MB) ra[q] = *reinterpret_cast<const uint32_t*>(smem + st + off_sa + q * 128);
+        else if (q < MB + NB) rb[q - MB] = *reinterpret_cast<const uint32_t*>(smem + st + off_sb + (q - MB) * 128);
+    };
     v16f acc[MB][NB];
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[m][n] = v16f{};
 
+    const int codes_first = min(NS - 1, nk);  // steps of codes among the first NS - 1
+    for (int st = 0; st < codes_first; ++st)
 #pragma unroll
-    for (int st = 0; st < TS_NS - 1; ++st) issue(st, min(st, nk - 1));
-    QE_WAIT_VMCNT_LDS((TS_NS - 2) * OPS);
-    QE_WG_BARRIER();
-    Frag f0, f1;
-    Scale s;
-    read(f0, 0, 0);
-    read_scales(s, 0);
-    for (int i = 0; i < nk; ++i) {
-        const int slot = i % TS_NS;
-        // refills the slot of step i - 1: every wave had its last fragments before the barrier below
-        // (past the end a repeat of the last step, never used)
-        issue((i + TS_NS - 1) % TS_NS, min(i + TS_NS - 1, nk - 1));
-        read(f1, slot, 1);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int c = 0; c < OPS; ++c) issue(c, lds0 + st * STAGE, st + 1 < nk);
+    if constexpr (TA) load_tokens();
+    const uint32_t present = __builtin_amdgcn_readfirstlane(s_present);
+    // adapter steps after the nk steps of codes: the shared expert's, then every present expert's
+    const int se = G.u && ky == 0 ? G.rs_pad / 32 : 0, re = G.rr_pad / 32;
+    const int nt = nk + se + __popc(present) * re;
+    // adapter step j (counted from the first step): its expert (-1: the shared one) and its operands' rows
+    struct Adapter {
+        int e, pad;
+        const uint16_t *x, *bt;
+    };
+    auto adapter = [&](int j) {
+        j -= nk;
+        if (j < se) return Adapter{-1, G.rs_pad, G.u + j * 32, G.bt_s + j * 32};
+        j -= se;
+        uint32_t left = present;
+        for (int q = j / re; q > 0; --q) left &= left - 1;
+        const int e = __builtin_ctz(left), k = j % re * 32;
+        return Adapter{e, G.rr_pad, G.v + k, G.bt_r + (size_t)e * G.d_out * G.rr_pad + k};
+    };
+    // copy c of an adapter step (the same number of copies as a step of codes: the scales' repeat theirs)
+    auto issue_adapter = [&](int c, uint32_t base, const Adapter& d) {
+        if (c < AD) {
+            const int q = wid + NW * c;
+            dma16(d.x + (size_t)s_tok[(q >> 1) * 32 + lr] * d.pad + (q & 1) * 16 + lh * 8, base + q * 1024);
+        } else if (c < AD + BD) {
+            const int q = wid + NW * (c - AD), ch = min(n0 + (q >> 1) * 32 + lr, G.d_out - 1);
+            dma16(d.bt + (size_t)ch * d.pad + (q & 1) * 16 + lh * 8, base + A_ST + q * 1024);
+        } else {
+            const int p = c - AD - BD;
+            dma4(s_src[p], base + A_ST + B_ST + (wid + NW * p) % SQ * 256);
+        }
+    };
+    for (int st = codes_first; st < NS - 1; ++st) {  // (few steps)
+        if (nt > nk) {
+            const Adapter d = adapter(min(st, nt - 1));
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+            for (int c = 0; c < OPS; ++c) issue_adapter(c, lds0 + st * STAGE, d);
+        } else {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) acc[m][n] = mx_mfma<0>(f0.a[m], s.a[m], f0.b[n], s.b[n], acc[m][n]);
-        __builtin_amdgcn_sched_barrier(0);
-        // step i + 1 has landed (later ones may be in flight) and this wave's reads of step i are done
-        QE_WAIT_VMCNT_LDS((TS_NS - 2) * OPS);
-        QE_WG_BARRIER();
-        Scale sn;
-        read(f0, (i + 1) % TS_NS, 0);
-        read_scales(sn, (i + 1) % TS_NS);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) acc[m][n] = mx_mfma<1>(f1.a[m], s.a[m], f1.b[n], s.b[n], acc[m][n]);
-        s = sn;
-    }
-    QE_WAIT_VMCNT(0);  // no copy may land after the workgroup has given its LDS back
-
-    // ---- adapter terms (of the first K split)
-    int tok[MB], ch[NB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) tok[m] = s_tok[(wm * MB + m) * 32 + lr];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) ch[n] = min(n0 + (wn * NB + n) * 32 + lr, G.d_out - 1);
-    if (G.u && ky == 0) {
-        for (int k = 0; k < G.rs_pad; k += 16) {
-            v8bf a[MB], b[NB];
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-                a[m] = *reinterpret_cast<const v8bf*>(G.u + (size_t)tok[m] * G.rs_pad + k + lh * 8);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-                b[n] = *reinterpret_cast<const v8bf*>(G.bt_s + (size_t)ch[n] * G.rs_pad + k + lh * 8);
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m], b[n], acc[m][n], 0, 0, 0);
+            for (int c = 0; c < OPS; ++c) issue(c, lds0 + st * STAGE, 0);
         }
     }
-    if (routed && ky == 0) {
-        int ex[MB];
-        uint32_t present = 0;  // experts of this wave's rows
+    int ex[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) ex[m] = s_ex[(wm * MB + m) * 32 + lr];
+    QE_WAIT_VMCNT_LDS((NS - 2) * OPS);
+    QE_WG_BARRIER();
+#pragma unroll
+    for (int q = 0; q < MB + NB; ++q) {
+        read(q, 0, 0, code_a[0]);
+        read_scale(q, 0);
+    }
+    constexpr int NM = MB * NB;  // MFMAs of a half step
+    constexpr int RQ = (MB + NB + NM - 1) / NM, CQ = (OPS + NM - 1) / NM;
+    int st = 0, st_next = STAGE, st_fill = (NS - 1) * STAGE;  // slots of steps i, i + 1 and i + NS - 1
+    // One step.  A wave issues in order, so whatever stands between two MFMAs for longer than one takes is
+    // lost to the matrix cores: reads and copies go one or two to an MFMA, fenced so that they stay there.
+    // kStep: 0 codes, copying codes; 1 codes, copying an adapter step; 2 adapter.  The slot refilled is that
+    // of step i - 1: every wave had its last fragments before the barrier (past the end: a repeat, never used).
+    auto step = [&](auto kind, int i) {
+        constexpr int kStep = decltype(kind)::value;
+        const int more = i + NS < nk;
+        int e = -1;
+        Adapter d;
+        if constexpr (kStep != 0) d = adapter(min(i + NS - 1, nt - 1));
+        if constexpr (kStep == 2) {
+            e = adapter(i).e;
+        } else {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) sa[m] = ra[m] >> (8 * lh);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) sb[n] = rb[n] >> (8 * lh);
+        }
+        auto mfma = [&](auto half, int q) {
+            constexpr int H = decltype(half)::value;
+            const int m = q / NB, n = q % NB;
+            if constexpr (kStep == 2) {
+                const v4i a = e < 0 || ex[m] == e ? fa[H][m] : v4i{0, 0, 0, 0};
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a),
+                                                                    __builtin_bit_cast(v8bf, fb[H][n]), acc[m][n], 0, 0, 0);
+            } else {
+                acc[m][n] = mx_mfma<H>(fa[H][m], sa[m], fb[H][n], sb[n], acc[m][n]);
+            }
+        };
+        const int here1 = kStep == 2 ? tile_a + 1024 : code_a[1];
+        const int next0 = kStep == 0 || (kStep == 1 && i + 1 < nk) ? code_a[0] : tile_a;
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mfma(std::integral_constant<int, 0>{}, q);
+#pragma unroll
+            for (int r = 0; r < RQ; ++r) read(q * RQ + r, st, 1, here1);
+#pragma unroll
+            for (int r = 0; r < CQ; ++r)
+                if (q * CQ + r < OPS) {
+                    if constexpr (kStep == 0) issue(q * CQ + r, lds0 + st_fill, more);
+                    else issue_adapter(q * CQ + r, lds0 + st_fill, d);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // step i + 1 has landed (later ones may be in flight) and this wave's reads of step i are done
+        QE_WAIT_VMCNT_LDS((NS - 2) * OPS);
+        QE_WG_BARRIER();
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mfma(std::integral_constant<int, 1>{}, q);
+#pragma unroll
+            for (int r = 0; r < RQ; ++r) {
+                read(q * RQ + r, st_next, 0, next0);
+                if constexpr (kStep != 2) read_scale(q * RQ + r, st_next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        st = st_next;
+        st_next = st_next == (NS - 1) * STAGE ? 0 : st_next + STAGE;
+        st_fill = st_fill == (NS - 1) * STAGE ? 0 : st_fill + STAGE;
+    };
+    int i = 0;
+    for (const int end = nt == nk ? nk : nk - (NS - 1); i < end; ++i) step(std::integral_constant<int, 0>{}, i);
+    for (; i < nk; ++i) step(std::integral_constant<int, 1>{}, i);
+    for (; i < nt; ++i) step(std::integral_constant<int, 2>{}, i);
+    QE_WAIT_VMCNT_LDS(0);  // no copy may land after the workgroup has given its LDS back
+
+    // ---- out: every wave turns one row of 32x32 blocks at a time into whole rows through its own part of
+    // the ring, and stores 16 bytes per lane, past the caches (nothing here reads y again)
+    QE_WG_BARRIER();  // the copies of every wave have landed
+    constexpr int COLS = NB * 32, PITCH = COLS * 4 + 16;  // channels and LDS bytes of a row
+    static_assert(NW * 32 * PITCH <= NS * STAGE, "the ring holds the waves' rows");
+    uint8_t* turn = smem + wid * 32 * PITCH;
+    const int c0 = n0 + wn * COLS;
+    auto out = [&](auto kind) {
+        constexpr int kOut = decltype(kind)::value;  // 0 partial sums, 1 float32, 2 bf16
+        constexpr int E = kOut == 2 ? 8 : 4, LPR = COLS / E, RPI = 64 / LPR;  // elements per lane, lanes per row, rows per store
+        float* base = kOut == 0 ? G.part + (size_t)ky * T * G.d_out : G.y;
+        const int c = lane % LPR * E;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            ex[m] = s_ex[(wm * MB + m) * 32 + lr];
-            for (int e = 0; e < G.n_r; ++e)
-                if (__ballot(ex[m] == e)) present |= 1u << e;
-        }
-        for (int k = 0; k < G.rr_pad; k += 16) {
-            v8bf a[MB];
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
-                a[m] = *reinterpret_cast<const v8bf*>(G.v + (size_t)tok[m] * G.rr_pad + k + lh * 8);
-            for (uint32_t left = present; left; left &= left - 1) {
-                const int e = __builtin_ctz(left);
-                v8bf b[NB];
+            for (int j = 0; j < 16; ++j)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-                    b[n] = *reinterpret_cast<const v8bf*>(G.bt_r + ((size_t)e * G.d_out + ch[n]) * G.rr_pad + k + lh * 8);
+                    *reinterpret_cast<float*>(turn + acc_row(j, lane) * PITCH + (n * 32 + lr) * 4) = acc[m][n][j];
 #pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    const v8bf am = ex[m] == e ? a[m] : v8bf{};
-#pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(am, b[n], acc[m][n], 0, 0, 0);
+            for (int j = 0; j < 32 / RPI; ++j) {
+                const int r = j * RPI + lane / LPR, q = (wm * MB + m) * 32 + r;
+                const v4f* p = reinterpret_cast<const v4f*>(turn + r * PITCH + c * 4);
+                const v4f lo = p[0];
+                if (m0 + q >= T || c0 + c >= G.d_out) continue;
+                const size_t o = (size_t)s_tok[q] * G.d_out + c0 + c;
+                if constexpr (kOut == 2) {
+                    const v4f hi = p[1];
+                    const v4u w = v4u{mx4_bf16_bits(lo[0]) | (mx4_bf16_bits(lo[1]) << 16),
+                                      mx4_bf16_bits(lo[2]) | (mx4_bf16_bits(lo[3]) << 16),
+                                      mx4_bf16_bits(hi[0]) | (mx4_bf16_bits(hi[1]) << 16),
+                                      mx4_bf16_bits(hi[2]) | (mx4_bf16_bits(hi[3]) << 16)};
+                    __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(base) + o));
+                } else if constexpr (kOut == 1) {
+                    __builtin_nontemporal_store(lo, reinterpret_cast<v4f*>(base + o));
+                } else {
+                    *reinterpret_cast<v4f*>(base + o) = lo;
                 }
             }
         }
-    }
-
-    // ---- out
-    float* part = ksplit > 1 ? G.part + (size_t)ky * T * G.d_out : nullptr;
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = (wm * MB + m) * 32 + acc_row(i, lane);
-            if (m0 + r >= T) continue;
-            const size_t row = (size_t)s_tok[r] * G.d_out;
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int c = n0 + (wn * NB + n) * 32 + lr;
-                if (c >= G.d_out) continue;
-                if (part) part[row + c] = acc[m][n][i];
-                else store_out(G.y, row + c, acc[m][n][i], G.y_bf16);
-            }
-        }
+    };
+    if (ksplit > 1) out(std::integral_constant<int, 0>{});
+    else if (G.y_bf16) out(std::integral_constant<int, 2>{});
+    else out(std::integral_constant<int, 1>{});
 }
 
 // ------------------------------------------------------------------ weight streaming
@@ -420,6 +504,14 @@ Mx4Plan mx4_plan(int T, int d_in, int d_out) {
     return P;
 }
 
+// Columns of 256-channel tiles for the large-tile launch: one tile runs per CU, so a last round that fills
+// few of the 256 CUs is given to 128 x 128 tiles instead (two per CU, a quarter of the work each).
+static int mx4_main_columns(int n_tm, int n_tn) {
+    const long n = (long)n_tm * n_tn, rounds = n / 256, rest = n - rounds * 256;
+    if (rounds == 0 || rest == 0 || rest > 96) return n_tn;
+    return (int)(rounds * 256 / n_tm);
+}
+
 hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
     if (G.T <= 0) return hipSuccess;
     if (P.kind == 0) {
@@ -427,11 +519,28 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
         if (G.T <= 32) hipLaunchKernelGGL(stream_mx4_kernel<1>, grid, block, 0, st, G, P.ksplit);
         else hipLaunchKernelGGL(stream_mx4_kernel<2>, grid, block, 0, st, G, P.ksplit);
     } else {
-        const int n_tm = (G.T + P.kind - 1) / P.kind, n_tn = (G.d_out + P.kind - 1) / P.kind;
-        const dim3 grid((unsigned)((size_t)n_tm * n_tn), P.ksplit);
-        if (P.kind == 256) hipLaunchKernelGGL((gemm_mx4_kernel<256, 256>), grid, dim3(256), 0, st, G, n_tm, P.ksplit);
-        else if (P.kind == 128) hipLaunchKernelGGL((gemm_mx4_kernel<128, 128>), grid, dim3(256), 0, st, G, n_tm, P.ksplit);
-        else hipLaunchKernelGGL((gemm_mx4_kernel<64, 64>), grid, dim3(256), 0, st, G, n_tm, P.ksplit);
+        Mx4Gemm H = G;
+        if (P.kind == 256) {
+            const hipError_t e = launch_mx4_prep(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
+            if (e != hipSuccess) return e;
+            H.codes = G.a_tiled;
+            H.scales = reinterpret_cast<const uint8_t*>(G.a_scale);
+            const int n_tm = (G.T + 255) / 256, n_tn = mx4_main_columns(n_tm, (G.d_out + 255) / 256);
+            hipLaunchKernelGGL((gemm_mx4_kernel<256, 256, 2, 4, true, 4>), dim3((unsigned)((size_t)n_tm * n_tn), P.ksplit),
+                               dim3(512), 0, st, H, n_tm, 0, P.ksplit);
+            if (n_tn * 256 < G.d_out) {
+                const int r_tm = (G.T + 127) / 128, r_tn = (G.d_out - n_tn * 256 + 127) / 128;
+                hipLaunchKernelGGL((gemm_mx4_kernel<128, 128, 2, 2, true, 4>), dim3((unsigned)((size_t)r_tm * r_tn), P.ksplit),
+                                   dim3(256), 0, st, H, r_tm, n_tn * 256, P.ksplit);
+            }
+        } else {
+            const int n_tm = (G.T + P.kind - 1) / P.kind, n_tn = (G.d_out + P.kind - 1) / P.kind;
+            const dim3 grid((unsigned)((size_t)n_tm * n_tn), P.ksplit);
+            if (P.kind == 128)
+                hipLaunchKernelGGL((gemm_mx4_kernel<128, 128, 2, 2, false, 4>), grid, dim3(256), 0, st, H, n_tm, 0, P.ksplit);
+            else
+                hipLaunchKernelGGL((gemm_mx4_kernel<64, 64, 2, 2, false, 4>), grid, dim3(256), 0, st, H, n_tm, 0, P.ksplit);
+        }
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || P.ksplit == 1) return e;

@@ -147,31 +147,32 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T
 // channel and K step, byte i the scale of its block i, ordered (channel block, K step, channel).
 // Channels past d_out (an odd number of 16-channel groups) hold zeros.
 __global__ __launch_bounds__(256) void mx4_prep_kernel(const uint8_t* __restrict__ codes,
-                                                       const uint8_t* __restrict__ scales, int d_out, int d_in,
-                                                       v4u* __restrict__ w_tiled, uint32_t* __restrict__ w_scale) {
-    const int KB = d_in / 128, NB = (d_out + 31) / 32;
+                                                       const uint8_t* __restrict__ scales,
+                                                       const int32_t* __restrict__ perm, int rows, int d_in,
+                                                       v4u* __restrict__ tiled, uint32_t* __restrict__ tiled_scale) {
+    const int KB = d_in / 128, NB = (rows + 31) / 32;
     const size_t n = (size_t)NB * KB * 128, stride = (size_t)gridDim.x * 256;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
         const int l = (int)(i & 63), h = (int)(i >> 6) & 1;
         const size_t q = i >> 7;
         const int nb = (int)(q / KB), kb = (int)(q - (size_t)nb * KB);
-        const int ch = nb * 32 + (l & 31);
+        const int pos = nb * 32 + (l & 31);
+        const size_t r = pos >= rows ? 0 : perm ? perm[pos] : pos;
         v4u c = v4u{0, 0, 0, 0};
-        if (ch < d_out)
-            c = *reinterpret_cast<const v4u*>(codes + (size_t)ch * (d_in / 2) + kb * 64 + h * 32 + (l >> 5) * 16);
-        w_tiled[i] = c;
+        if (pos < rows) c = *reinterpret_cast<const v4u*>(codes + r * (d_in / 2) + kb * 64 + h * 32 + (l >> 5) * 16);
+        tiled[i] = c;
         if (h == 0 && l < 32)
-            w_scale[q * 32 + l] =
-                ch < d_out ? *reinterpret_cast<const uint32_t*>(scales + (size_t)ch * (d_in / 32) + kb * 4) : 0u;
+            tiled_scale[q * 32 + l] =
+                pos < rows ? *reinterpret_cast<const uint32_t*>(scales + r * (d_in / 32) + kb * 4) : 0u;
     }
 }
 
-hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, int d_out, int d_in, uint8_t* w_tiled,
-                           uint32_t* w_scale, hipStream_t st) {
-    const size_t n = (size_t)((d_out + 31) / 32) * (d_in / 128) * 128;
+hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
+                           uint8_t* tiled, uint32_t* tiled_scale, hipStream_t st) {
+    const size_t n = (size_t)((rows + 31) / 32) * (d_in / 128) * 128;
     const unsigned grid = (unsigned)std::min<size_t>((n + 255) / 256, 256 * 32);
-    hipLaunchKernelGGL(mx4_prep_kernel, dim3(grid), dim3(256), 0, st, codes, scales, d_out, d_in,
-                       reinterpret_cast<v4u*>(w_tiled), w_scale);
+    hipLaunchKernelGGL(mx4_prep_kernel, dim3(grid), dim3(256), 0, st, codes, scales, perm, rows, d_in,
+                       reinterpret_cast<v4u*>(tiled), tiled_scale);
     return hipGetLastError();
 }
 

@@ -157,11 +157,10 @@ PrepLayout prep_layout(const qe_linear* lin) {
     L.n_cols_pad = (L.n_cols + 15) / 16 * 16;
     size_t off = 0;
     L.w_tiled = off;
-    const size_t d_out32 = (d_out + 31) / 32 * 32;  // the microscaled tiles hold whole 32-channel blocks
-    L.w_tiled_bytes = mx4(lin) ? d_out32 * d_in / 2 : lin->w_bits == 4 ? d_out * d_in / 2 : d_out * d_in * 3 / 8;
+    L.w_tiled_bytes = mx4(lin) ? mx4_tile_codes(d_out, d_in) : lin->w_bits == 4 ? d_out * d_in / 2 : d_out * d_in * 3 / 8;
     off = align256(off + L.w_tiled_bytes);
     L.w_scale = off;
-    off = align256(off + (mx4(lin) ? d_out32 * d_in / kMxBlock : d_out * 4));
+    off = align256(off + (mx4(lin) ? mx4_tile_scales(d_out, d_in) : d_out * 4));
     L.smooth = off;
     off = align256(off + (L.has_smooth ? d_in * 4 : 0));
     L.inv_smooth = off;
@@ -222,6 +221,11 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     const int skinny_parts = mx4(lin) && W.skinny_ksplit == 1 ? 0 : W.skinny_ksplit;
     off = align256(off + (size_t)std::max({skinny_parts, D.ks_m, W.gemm_ksplit > 1 ? W.gemm_ksplit : 0}) * t *
                              lin->d_out * 4);
+    const bool tiles = mx4(lin) && mx4_plan(T, lin->d_in, lin->d_out).kind == 256;
+    W.a_tiled = off;
+    off = align256(off + (tiles ? mx4_tile_codes(t, lin->d_in) : 0));
+    W.a_scale = off;
+    off = align256(off + (tiles ? mx4_tile_scales(t, lin->d_in) : 0));
     W.total = off;
     return W;
 }
@@ -411,7 +415,7 @@ int qe_mx4_prepare(const qe_linear* lin, const uint8_t* w_codes, const uint8_t* 
         QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
     const PrepLayout L = prep_layout(lin);
     hipStream_t s = S(stream);
-    QE_TRY_HIP(launch_mx4_prep(w_codes, w_scales, lin->d_out, lin->d_in, at<uint8_t>(prep, L.w_tiled),
+    QE_TRY_HIP(launch_mx4_prep(w_codes, w_scales, nullptr, lin->d_out, lin->d_in, at<uint8_t>(prep, L.w_tiled),
                                at<uint32_t>(prep, L.w_scale), s));
     return prepare_rest(lin, smooth, A_s, B_s, A_r, B_r, R, prep, s);
 }
@@ -621,7 +625,10 @@ static int run_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_
     }
     G.perm = perm;
     G.y = y;
-    G.part = plan.ksplit > 1 ? at<float>(ws, ws_layout(lin, T).skinny) : nullptr;
+    const WsLayout W = ws_layout(lin, T);
+    G.part = plan.ksplit > 1 ? at<float>(ws, W.skinny) : nullptr;
+    G.a_tiled = at<uint8_t>(ws, W.a_tiled);
+    G.a_scale = at<uint32_t>(ws, W.a_scale);
     G.T = T;
     G.d_in = lin->d_in;
     G.d_out = lin->d_out;

@@ -86,6 +86,7 @@ struct WsLayout {
     int skinny_ksplit;
     size_t vpart;       // float [eq_ksplit][T][rr_pad] (expert-quant split-K partials)
     int rp_ksplit, eq_ksplit;  // 0 unless the two-pass prefill prologue is used
+    size_t a_tiled, a_scale;   // microscaled products of many tokens: the activations' tiles
     int gemm_ksplit;           // K splits of the A6/A8 main product (partials in `skinny`)
 };
 

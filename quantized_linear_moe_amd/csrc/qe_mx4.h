@@ -71,9 +71,13 @@ hipError_t launch_mx4_quant(const void* x, int x_dtype, const float* smooth, boo
                             uint8_t* codes, uint8_t* scales, hipStream_t st);
 hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T, int d, void* x, int x_dtype,
                               hipStream_t st);
-// canonical codes and scales of [d_out][d_in] weights into the product's tiles (see k_mx4.hip)
-hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, int d_out, int d_in, uint8_t* w_tiled,
-                           uint32_t* w_scale, hipStream_t st);
+// canonical codes and scales of [rows][d_in] into the product's tiles (see k_mx4.hip), rows in the
+// order of `perm` when it is given
+hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
+                           uint8_t* tiled, uint32_t* tiled_scale, hipStream_t st);
+// bytes of the tiles of [rows][d_in] (codes, scales)
+inline size_t mx4_tile_codes(size_t rows, size_t d_in) { return (rows + 31) / 32 * 32 * d_in / 2; }
+inline size_t mx4_tile_scales(size_t rows, size_t d_in) { return (rows + 31) / 32 * 32 * d_in / kMxBlock; }
 
 // How the product runs for T tokens: which kernel and how many K splits (more than one: float32
 // partials [ksplit][T][d_out] in the workspace, added by a finish kernel)
@@ -96,6 +100,8 @@ struct Mx4Gemm {
     const int32_t* perm;       // [T] or NULL
     float* y;                  // [T][d_out] (bf16 elements when y_bf16)
     float* part;               // [ksplit][T][d_out] when ksplit > 1
+    uint8_t* a_tiled;          // workspace for the activations' tiles (256-token tiles)
+    uint32_t* a_scale;
     int T, d_in, d_out, rs_pad, rr_pad, n_r;
     bool y_bf16;
 };
