@@ -12,6 +12,7 @@ import os
 from typing import Optional
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqe.so")
@@ -140,7 +141,6 @@ def _ptr(t) -> Optional[int]:
 
 
 def _dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.bfloat16:
         return QE_BF16
     if t.dtype == torch.float32:
@@ -149,7 +149,6 @@ def _dtype_code(t) -> int:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
@@ -296,41 +295,42 @@ def qe_linear_forward_noalloc(lin, x, y, expert_out, stream=None):
                                           _ptr(expert_out), _stream(stream)), "qe_linear_forward_noalloc")
 
 
-def _on(where, first, *rest):
+def _on(where, *args):
     """Checks the arguments of a device call: (name, tensor, shape, dtype) each, tensor None where it
     may be left out; all dense, on the device of the first.  Returns that device's index."""
-    dev = first[1].device
-    for name, t, shape, dtype in (first, *rest):
+    index = args[0][1].get_device()
+    for name, t, shape, dtype in args:
         if t is None:
             continue
         if t.dtype != dtype:
             raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{where}: {name} must have shape {shape}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
-        if t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, not {dev}")
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: needs device tensors, got {dev}")
-    return dev.index
+        if t.get_device() != index:
+            raise ValueError(f"{where}: {name} is on {t.device}, not {args[0][1].device}")
+    if index < 0:
+        raise ValueError(f"{where}: needs device tensors, got {args[0][1].device}")
+    return index
 
 
 def _call_on(index, where, fn, *args, stream=None):
     """fn(*args, stream) with the tensors' device current, on `stream` or that device's current one."""
-    import torch
+    # the raw handle: making a torch.cuda.Stream for it takes as long as a small launch
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+        st = fn(*args, s)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _stream(stream))
-    _check(st, where)
+            st = fn(*args, s)
+    if st != QE_OK:
+        raise QEError(st, where)
 
 
 def qe_mx4_quant(x, smooth, codes, scales, multiply=False, stream=None):
     """Enqueue the microscaled 4-bit form of x / smooth (multiply: x * smooth; smooth may be None):
     codes uint8 [T, d // 2], scales uint8 [T, d // 32]."""
-    import torch
     T, d = x.shape
     dev = _on("qe_mx4_quant", ("x", x, (T, d), x.dtype), ("smooth", smooth, (d,), torch.float32),
               ("codes", codes, (T, d // 2), torch.uint8), ("scales", scales, (T, d // 32), torch.uint8))
@@ -340,7 +340,6 @@ def qe_mx4_quant(x, smooth, codes, scales, multiply=False, stream=None):
 
 def qe_mx4_dequant(codes, scales, x, stream=None):
     """Enqueue x (bf16 or float32 [T, d]) = the values of microscaled codes and scales."""
-    import torch
     T, d = x.shape
     dev = _on("qe_mx4_dequant", ("x", x, (T, d), x.dtype), ("codes", codes, (T, d // 2), torch.uint8),
               ("scales", scales, (T, d // 32), torch.uint8))
@@ -350,7 +349,6 @@ def qe_mx4_dequant(codes, scales, x, stream=None):
 
 def qe_mx4_prepare(lin: qe_linear, w_codes, w_scales, smooth, A_s, B_s, A_r, B_r, R, prep, stream=None):
     """qe_prepare for a linear with a_bits 4 (w_codes, w_scales: qe_mx4_quant of its weights)."""
-    import torch
     bf, i, o, rs, n, rr = torch.bfloat16, lin.d_in, lin.d_out, lin.r_shared, lin.n_routed, lin.r_routed
     dev = _on("qe_mx4_prepare", ("w_codes", w_codes, (o, i // 2), torch.uint8),
               ("w_scales", w_scales, (o, i // 32), torch.uint8), ("smooth", smooth, (i,), torch.float32),
@@ -366,7 +364,6 @@ def qe_mx4_prepare(lin: qe_linear, w_codes, w_scales, smooth, A_s, B_s, A_r, B_r
 def qe_mx4_gemm(lin: qe_linear, codes, scales, u, v, expert, y, ws, perm=None, stream=None):
     """Enqueue y = the product of microscaled activations [T, d_in] and the prepared weights, plus the
     shared (u) and routed (v, expert) low-rank terms where given (rows padded to rank_pad)."""
-    import torch
     T = codes.shape[0]
     dev = _on("qe_mx4_gemm", ("codes", codes, (T, lin.d_in // 2), torch.uint8),
               ("scales", scales, (T, lin.d_in // 32), torch.uint8),
@@ -382,7 +379,6 @@ def qe_mx4_gemm(lin: qe_linear, codes, scales, u, v, expert, y, ws, perm=None, s
 def qe_add_rmsnorm(x, res, weight, eps, h=None, xn=None, smooth=None, a_bits=0, codes=None, scales=None, stream=None):
     """Enqueue h = x + res (res may be None), xn = RMS norm of h times weight, and with a_bits 4, 6 or 8
     the codes and scales of xn / smooth (see include/qe.h; outputs left out are None)."""
-    import torch
     T, d = x.shape
     mx = a_bits == 4
     dev = _on("qe_add_rmsnorm", ("x", x, (T, d), x.dtype), ("res", res, (T, d), x.dtype),
