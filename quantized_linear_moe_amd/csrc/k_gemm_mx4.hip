@@ -51,24 +51,28 @@ __device__ inline void store_out(float* y, size_t idx, float v, bool y_bf16) {
 // that frees a ring slot stands between the two halves of a step, when the second half's fragments are
 // already in registers: the matrix cores meet it with work at hand.
 //
-// Adapter terms are more steps of the same ring: 32 ranks of u (or v) and of B_s (or of one expert's
-// B_e) have the bytes of 128 codes and the same fragments, 16 ranks per half, multiplied in bf16.  A
-// routed step is masked to its expert's rows; only experts that some row of the tile uses are met.
+// Adapter terms are more steps of the same ring: a row's 32 ranks of u (or v) and of B_s (or of one
+// expert's B_e) have the 64 bytes of 128 codes, 16 ranks per half, multiplied in bf16.  A routed step is
+// masked to its expert's rows; only experts that some row of the tile uses are met.
 //
-// TA: the activations come as tiles like the weights (mx4_prep_kernel, in the order of perm): every
-// copy is contiguous.  Otherwise from their rows: the code rows of a step are 64 bytes, four chunks of 16
-// stored at chunk ^ ((row >> 1) & 3), so that neighbouring rows lie in different banks.
+// Operands that come as rows (adapters; activations unless TA) are copied 16 rows of 64 bytes at a time,
+// a row's four chunks of 16 stored at chunk ^ ((row >> 2) & 3), so that the fragment reads of 16
+// neighbouring rows reach all 64 banks.  TA: the activations come as tiles like the weights
+// (mx4_prep_kernel, in the order of perm), every copy contiguous.  Otherwise their scales, one dword per row
+// and step, are copied four steps at a time, 16 rows per copy, into four slots of their own: step by step
+// every row's dword would be a memory request of its own, as many as the codes make.
 template <int BM, int BN, int WM, int WN, bool TA, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, int n_tm, int n_off, int ksplit) {
     constexpr int NW = WM * WN;
     constexpr int MB = BM / 32 / WM, NB = BN / 32 / WN;    // 32x32 blocks per wave
     constexpr int A_ST = BM * 64, B_ST = BN * 64;          // codes per step
-    constexpr int STAGE = A_ST + B_ST + BM * 4 + BN * 4;   // + scales
+    constexpr int A_SC = TA ? BM * 4 : 0, STAGE = A_ST + B_ST + A_SC + BN * 4;  // + scales
+    constexpr int ROWSC = NS * STAGE, ROWSC_SLOT = TA ? 0 : BM * 16;  // scales by rows: 4 slots of 4 steps
     constexpr int AD = BM / 16 / NW, BD = BN / 16 / NW;    // 1 KB copies per wave
     constexpr int SQ = BM / 64 + BN / 64, SD = (SQ + NW - 1) / NW;  // 256-byte scale copies: in all, per wave
     constexpr int OPS = AD + BD + SD;
     static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "whole copies per wave");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[ROWSC + 4 * ROWSC_SLOT];
     __shared__ int s_tok[BM];  // the token of every row (its position in tiled form is the row's own)
     __shared__ int s_ex[BM];   // its routed expert, -1 past the last token
     __shared__ uint32_t s_present;
@@ -94,59 +98,35 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
     const int kb0 = (int)((long)ky * KB / ksplit), nk = (int)((long)(ky + 1) * KB / ksplit) - kb0;
     const bool routed = G.v != nullptr && ky == 0;  // the first K split has the adapter terms
 
-    // The tile's tokens and routed experts.  Copies from tiles do not wait for them, so there they are
-    // loaded behind the first copies.
-    auto load_tokens = [&]() {
-        if (tid == 0) s_present = 0;
-        __syncthreads();
-        for (int r = tid; r < BM; r += 64 * NW) {
-            const int pos = min(m0 + r, T - 1);
-            const int tk = G.perm ? G.perm[pos] : pos;
-            const int e = (routed && m0 + r < T) ? min(max(G.expert[tk], 0), G.n_r - 1) : -1;
-            s_tok[r] = tk;
-            s_ex[r] = e;
-            if (e >= 0) atomicOr(&s_present, 1u << e);
-        }
-        __syncthreads();
-    };
-    if constexpr (!TA) load_tokens();
-
     const uint32_t lds0 = lds_addr(smem);
-    const uint8_t *a_src[AD], *b_src[BD], *s_src[SD];
-#pragma unroll
-    for (int p = 0; p < AD; ++p) {
-        const int q = wid + NW * p;
-        if constexpr (TA) {  // as for B below
-            const int mb = min(m0 / 32 + (q >> 1), NBA - 1);
-            a_src[p] = G.codes + (((size_t)mb * KB + kb0) * 2 + (q & 1)) * 1024 + lane * 16;
-        } else {  // rows 16q..16q+15: lane i fetches the chunk stored at slot i%4
-            const int r = 16 * q + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
-            a_src[p] = G.codes + (size_t)s_tok[r] * (G.d_in / 2) + (size_t)kb0 * 64 + c * 16;
-        }
-    }
+    const int row_chunk = (lane & 3) ^ ((lane >> 4) & 3);  // of row lane / 4, the chunk that slot lane % 4 holds
+    const uint8_t *a_src[AD], *b_src[BD], *s_src[SD], *r_src[SD][4];
+    auto scale_copy = [&](int p) { return (wid + NW * p) % SQ; };  // fewer copies than waves: repeated, the same bytes
 #pragma unroll
     for (int p = 0; p < BD; ++p) {  // B copy q: half step q & 1 of channel block q >> 1
         const int q = wid + NW * p, nb = min(n0 / 32 + (q >> 1), NBT - 1);
         b_src[p] = G.w_tiled + (((size_t)nb * KB + kb0) * 2 + (q & 1)) * 1024 + lane * 16;
     }
-    int s_step[SD];  // scale copies: 64 rows of A each, then 64 channels of B each
 #pragma unroll
-    for (int p = 0; p < SD; ++p) {
-        const int q = (wid + NW * p) % SQ;  // fewer copies than waves: repeated, the same bytes
-        s_step[p] = 128;
+    for (int p = 0; p < SD; ++p) {  // scale copies: 64 rows of A each, then 64 channels of B each
+        const int q = scale_copy(p);
         if (q >= BM / 64) {
             const int nb = min(n0 / 32 + (q - BM / 64) * 2 + lh, NBT - 1);
             s_src[p] = reinterpret_cast<const uint8_t*>(G.w_scale + ((size_t)nb * KB + kb0) * 32 + lr);
-        } else if (TA) {
-            const int mb = min(m0 / 32 + q * 2 + lh, NBA - 1);
-            s_src[p] = G.scales + ((size_t)mb * KB + kb0) * 128 + lr * 4;
         } else {
-            s_src[p] = G.scales + (size_t)s_tok[q * 64 + lane] * (G.d_in / 32) + (size_t)kb0 * 4;
-            s_step[p] = 4;
+            const int mb = min(m0 / 32 + q * 2 + lh, NBA - 1);
+            s_src[p] = G.scales + ((size_t)mb * KB + kb0) * 128 + lr * 4;  // (TA)
         }
     }
-    // copy c of a step of codes into the ring slot at LDS address `base`; its source moves on (more != 0)
-    auto issue = [&](int c, uint32_t base, int more) {
+    // scales by rows: quarter k (16 rows) of copy p for the steps 4g..4g+3 (past the end: the last step's)
+    auto issue_row_scales = [&](int p, int k, int g) {
+        const uint8_t* src = k == 0 ? r_src[p][0] : k == 1 ? r_src[p][1] : k == 2 ? r_src[p][2] : r_src[p][3];
+        dma4(src + 4 * min(4 * g + (lane & 3), nk - 1), lds0 + ROWSC + (g & 3) * ROWSC_SLOT + (scale_copy(p) * 64 + k * 16) * 16);
+    };
+    // copy c of step j of the codes into the ring slot at LDS address `base` (AD of A, BD of B, SD of scales);
+    // its source moves on (more != 0).  Of the scales by rows, step j copies a quarter of the group of four
+    // steps after its own.
+    auto issue = [&](int c, uint32_t base, int more, int j) {
         if (c < AD) {
             dma16(a_src[c], base + (wid + NW * c) * 1024);
             a_src[c] += more * (TA ? 2048 : 64);
@@ -155,89 +135,162 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
             dma16(b_src[p], base + A_ST + (wid + NW * p) * 1024);
             b_src[p] += more * 2048;
         } else {
-            const int p = c - AD - BD;
-            dma4(s_src[p], base + A_ST + B_ST + (wid + NW * p) % SQ * 256);
-            s_src[p] += more * s_step[p];
+            const int p = c - AD - BD, q = scale_copy(p);
+            if (!TA && q < BM / 64) {
+                issue_row_scales(p, j & 3, (j >> 2) + 1);
+            } else {
+                dma4(s_src[p], base + A_ST + B_ST + (q - (TA ? 0 : BM / 64)) * 256);
+                s_src[p] += more * 128;
+            }
         }
     };
+    const int first = min(NS - 1, nk);  // steps of codes among the first NS - 1 of the ring
+    // The tile's tokens, then their routed experts.  Copies that do not wait for them go first: the
+    // weights, and tiled activations.
+    auto issue_first = [&](int c0, int c1) {
+        for (int st = 0; st < first; ++st)
+#pragma unroll
+            for (int c = 0; c < OPS; ++c)
+                if (c >= c0 && c < c1) issue(c, lds0 + st * STAGE, st + 1 < nk, st);
+    };
+    if constexpr (TA) {
+#pragma unroll
+        for (int p = 0; p < AD; ++p) {
+            const int q = wid + NW * p, mb = min(m0 / 32 + (q >> 1), NBA - 1);
+            a_src[p] = G.codes + (((size_t)mb * KB + kb0) * 2 + (q & 1)) * 1024 + lane * 16;
+        }
+        issue_first(0, OPS);
+    } else {
+        issue_first(AD, AD + BD);
+    }
+    if (tid == 0) s_present = 0;
+    for (int r = tid; r < BM; r += 64 * NW) {
+        const int pos = min(m0 + r, T - 1);
+        s_tok[r] = G.perm ? G.perm[pos] : pos;
+    }
+    QE_WAIT_LDS();  // (no __syncthreads: it would also wait for the copies)
+    QE_WG_BARRIER();
+    if constexpr (!TA) {
+#pragma unroll
+        for (int p = 0; p < AD; ++p)
+            a_src[p] = G.codes + (size_t)s_tok[16 * (wid + NW * p) + (lane >> 2)] * (G.d_in / 2) + (size_t)kb0 * 64 + row_chunk * 16;
+#pragma unroll
+        for (int p = 0; p < SD; ++p) {
+            const int q = scale_copy(p);
+            if (q >= BM / 64) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                r_src[p][k] = G.scales + (size_t)s_tok[q * 64 + k * 16 + (lane >> 2)] * (G.d_in / 32) + (size_t)kb0 * 4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) issue_row_scales(p, k, 0);
+        }
+        issue_first(0, AD);
+        issue_first(AD + BD, OPS);
+    }
+    if (routed) {
+        for (int r = tid; r < BM; r += 64 * NW) {
+            const int e = m0 + r < T ? min(max(G.expert[s_tok[r]], 0), G.n_r - 1) : -1;
+            s_ex[r] = e;
+            if (e >= 0) atomicOr(&s_present, 1u << e);
+        }
+        QE_WAIT_LDS();
+        QE_WG_BARRIER();
+    }
+    const uint32_t present = __builtin_amdgcn_readfirstlane(s_present);
+    // Adapter steps follow the nk steps of codes: the shared expert's, then those of every present expert in
+    // turn.  `turn` walks them; the experts of the steps in the ring wait in `queue`.
+    const int se = G.u && ky == 0 ? G.rs_pad / 32 : 0, re = G.rr_pad / 32;
+    const int nt = nk + se + __popc(present) * re;
+    struct {
+        int s, k;
+        uint32_t left;
+    } turn = {0, 0, present};
+    int queue[NS];
+    const uint16_t *ad_x, *ad_bt;  // the rows of the adapter step being copied
+    int ad_pad;
+    int ad_tok[AD], ad_ch[BD];
+#pragma unroll
+    for (int p = 0; p < AD; ++p) ad_tok[p] = s_tok[16 * (wid + NW * p) + (lane >> 2)];
+#pragma unroll
+    for (int p = 0; p < BD; ++p) ad_ch[p] = min(n0 + 16 * (wid + NW * p) + (lane >> 2), G.d_out - 1);
+    auto next_adapter = [&]() {  // (after the last one: the last again, into slots that nothing reads)
+        int e = -1;
+        if (turn.s < se) {
+            ad_x = G.u + turn.s * 32;
+            ad_bt = G.bt_s + turn.s * 32;
+            ad_pad = G.rs_pad;
+            ++turn.s;
+        } else if (turn.left) {
+            e = __builtin_ctz(turn.left);
+            ad_x = G.v + turn.k;
+            ad_bt = G.bt_r + (size_t)e * G.d_out * G.rr_pad + turn.k;
+            ad_pad = G.rr_pad;
+            turn.k += 32;
+            if (turn.k == G.rr_pad) {
+                turn.k = 0;
+                turn.left &= turn.left - 1;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q + 1 < NS; ++q) queue[q] = queue[q + 1];
+        queue[NS - 1] = e;
+    };
+    // copy c of that step (the scales' are repeated: every step makes the same number of copies)
+    auto issue_adapter = [&](int c, uint32_t base, int j) {
+        if (c < AD) dma16(ad_x + (size_t)ad_tok[c] * ad_pad + row_chunk * 8, base + (wid + NW * c) * 1024);
+        else if (c < AD + BD) dma16(ad_bt + (size_t)ad_ch[c - AD] * ad_pad + row_chunk * 8, base + A_ST + (wid + NW * (c - AD)) * 1024);
+        else issue(c, base, 0, j);
+    };
+    for (int st = first; st < NS - 1; ++st) {  // (fewer steps of codes than the ring holds)
+        if (nt > nk) {
+            next_adapter();
+#pragma unroll
+            for (int c = 0; c < OPS; ++c) issue_adapter(c, lds0 + st * STAGE, st);
+        } else {
+#pragma unroll
+            for (int c = 0; c < OPS; ++c) issue(c, lds0 + st * STAGE, 0, st);
+        }
+    }
+    int ex[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) ex[m] = routed ? s_ex[(wm * MB + m) * 32 + lr] : -1;
+
     // fragments and scales of the slot at offset `st`, numbered so that their reads can be spread between
-    // MFMAs: MB of A, then NB of B.  off: the A fragments' place (adapter steps are always in tile order)
+    // MFMAs: MB of A, then NB of B.  offa, offb: the fragments' places, as tiles or as rows
     v4i fa[2][MB], fb[2][NB];
     uint32_t ra[MB], rb[NB], sa[MB], sb[NB];  // scale dwords as read, and with the lane's blocks in bytes 0 and 2
-    const int tile_a = wm * MB * 2048 + lane * 16, off_b = A_ST + wn * NB * 2048 + lane * 16;
-    const int row_a = (wm * MB * 32 + lr) * 64, row_swz = (lr >> 1) & 3;
-    const int code_a[2] = {TA ? tile_a : row_a + ((lh ^ row_swz) << 4), TA ? tile_a + 1024 : row_a + (((2 + lh) ^ row_swz) << 4)};
-    const int off_sa = A_ST + B_ST + (wm * MB * 32 + lr) * 4, off_sb = A_ST + B_ST + BM * 4 + (wn * NB * 32 + lr) * 4;
-    auto read = [&](int q, int st, int h, int off) {
-        if (q < MB) fa[h][q] = *reinterpret_cast<const v4i*>(smem + st + off + q * 2048);
-        else if (q < MB + NB)
-            fb[h][q - MB] = *reinterpret_cast<const v4i*>(smem + st + off_b + (q - MB) * 2048 + h * 1024);
+    const int swz = (lr >> 2) & 3, rows_a = (wm * MB * 32 + lr) * 64, rows_b = A_ST + (wn * NB * 32 + lr) * 64;
+    const int row_a[2] = {rows_a + ((lh ^ swz) << 4), rows_a + (((2 + lh) ^ swz) << 4)};
+    const int row_b[2] = {rows_b + ((lh ^ swz) << 4), rows_b + (((2 + lh) ^ swz) << 4)};
+    const int tile_a = wm * MB * 2048 + lane * 16, tile_b = A_ST + wn * NB * 2048 + lane * 16;
+    const int code_a[2] = {TA ? tile_a : row_a[0], TA ? tile_a + 1024 : row_a[1]}, code_b[2] = {tile_b, tile_b + 1024};
+    const int off_sa = TA ? A_ST + B_ST + (wm * MB * 32 + lr) * 4 : ROWSC + (wm * MB * 32 + lr) * 16;
+    const int off_sb = A_ST + B_ST + A_SC + (wn * NB * 32 + lr) * 4;
+    auto read = [&](int q, int st, int h, int offa, int offb) {
+        if (q < MB) fa[h][q] = *reinterpret_cast<const v4i*>(smem + st + offa + q * 2048);
+        else if (q < MB + NB) fb[h][q - MB] = *reinterpret_cast<const v4i*>(smem + st + offb + (q - MB) * 2048);
     };
-    auto read_scale = [&](int q, int st) {
-        if (q < MB) ra[q] = *reinterpret_cast<const uint32_t*>(smem + st + off_sa + q * 128);
-        else if (q < MB + NB) rb[q - MB] = *reinterpret_cast<const uint32_t*>(smem + st + off_sb + (q - MB) * 128);
+    auto read_scale = [&](int q, int st, int j) {  // of step j
+        if (q < MB) {
+            const int o = TA ? st + q * 128 : ((j >> 2) & 3) * ROWSC_SLOT + (j & 3) * 4 + q * 512;
+            ra[q] = *reinterpret_cast<const uint32_t*>(smem + off_sa + o);
+        } else if (q < MB + NB) {
+            rb[q - MB] = *reinterpret_cast<const uint32_t*>(smem + st + off_sb + (q - MB) * 128);
+        }
     };
+
     v16f acc[MB][NB];
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int n = 0; n < NB; ++n) acc[m][n] = v16f{};
 
-    const int codes_first = min(NS - 1, nk);  // steps of codes among the first NS - 1
-    for (int st = 0; st < codes_first; ++st)
-#pragma unroll
-        for (int c = 0; c < OPS; ++c) issue(c, lds0 + st * STAGE, st + 1 < nk);
-    if constexpr (TA) load_tokens();
-    const uint32_t present = __builtin_amdgcn_readfirstlane(s_present);
-    // adapter steps after the nk steps of codes: the shared expert's, then every present expert's
-    const int se = G.u && ky == 0 ? G.rs_pad / 32 : 0, re = G.rr_pad / 32;
-    const int nt = nk + se + __popc(present) * re;
-    // adapter step j (counted from the first step): its expert (-1: the shared one) and its operands' rows
-    struct Adapter {
-        int e, pad;
-        const uint16_t *x, *bt;
-    };
-    auto adapter = [&](int j) {
-        j -= nk;
-        if (j < se) return Adapter{-1, G.rs_pad, G.u + j * 32, G.bt_s + j * 32};
-        j -= se;
-        uint32_t left = present;
-        for (int q = j / re; q > 0; --q) left &= left - 1;
-        const int e = __builtin_ctz(left), k = j % re * 32;
-        return Adapter{e, G.rr_pad, G.v + k, G.bt_r + (size_t)e * G.d_out * G.rr_pad + k};
-    };
-    // copy c of an adapter step (the same number of copies as a step of codes: the scales' repeat theirs)
-    auto issue_adapter = [&](int c, uint32_t base, const Adapter& d) {
-        if (c < AD) {
-            const int q = wid + NW * c;
-            dma16(d.x + (size_t)s_tok[(q >> 1) * 32 + lr] * d.pad + (q & 1) * 16 + lh * 8, base + q * 1024);
-        } else if (c < AD + BD) {
-            const int q = wid + NW * (c - AD), ch = min(n0 + (q >> 1) * 32 + lr, G.d_out - 1);
-            dma16(d.bt + (size_t)ch * d.pad + (q & 1) * 16 + lh * 8, base + A_ST + q * 1024);
-        } else {
-            const int p = c - AD - BD;
-            dma4(s_src[p], base + A_ST + B_ST + (wid + NW * p) % SQ * 256);
-        }
-    };
-    for (int st = codes_first; st < NS - 1; ++st) {  // (few steps)
-        if (nt > nk) {
-            const Adapter d = adapter(min(st, nt - 1));
-#pragma unroll
-            for (int c = 0; c < OPS; ++c) issue_adapter(c, lds0 + st * STAGE, d);
-        } else {
-#pragma unroll
-            for (int c = 0; c < OPS; ++c) issue(c, lds0 + st * STAGE, 0);
-        }
-    }
-    int ex[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) ex[m] = s_ex[(wm * MB + m) * 32 + lr];
-    QE_WAIT_VMCNT_LDS((NS - 2) * OPS);
+    QE_WAIT_VMCNT_LDS(TA ? (NS - 2) * OPS : 0);  // rows: the first copies were not issued step by step
     QE_WG_BARRIER();
 #pragma unroll
     for (int q = 0; q < MB + NB; ++q) {
-        read(q, 0, 0, code_a[0]);
-        read_scale(q, 0);
+        read(q, 0, 0, code_a[0], code_b[0]);
+        read_scale(q, 0, 0);
     }
     constexpr int NM = MB * NB;  // MFMAs of a half step
     constexpr int RQ = (MB + NB + NM - 1) / NM, CQ = (OPS + NM - 1) / NM;
@@ -250,10 +303,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
         constexpr int kStep = decltype(kind)::value;
         const int more = i + NS < nk;
         int e = -1;
-        Adapter d;
-        if constexpr (kStep != 0) d = adapter(min(i + NS - 1, nt - 1));
+        if constexpr (kStep != 0) next_adapter();  // step i's own expert is now first in the queue
         if constexpr (kStep == 2) {
-            e = adapter(i).e;
+            e = queue[0];
         } else {
 #pragma unroll
             for (int m = 0; m < MB; ++m) sa[m] = ra[m] >> (8 * lh);
@@ -271,18 +323,19 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
                 acc[m][n] = mx_mfma<H>(fa[H][m], sa[m], fb[H][n], sb[n], acc[m][n]);
             }
         };
-        const int here1 = kStep == 2 ? tile_a + 1024 : code_a[1];
-        const int next0 = kStep == 0 || (kStep == 1 && i + 1 < nk) ? code_a[0] : tile_a;
+        const int here_a = kStep == 2 ? row_a[1] : code_a[1], here_b = kStep == 2 ? row_b[1] : code_b[1];
+        const bool codes_next = kStep == 0 || (kStep == 1 && i + 1 < nk);
+        const int next_a = codes_next ? code_a[0] : row_a[0], next_b = codes_next ? code_b[0] : row_b[0];
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
             mfma(std::integral_constant<int, 0>{}, q);
 #pragma unroll
-            for (int r = 0; r < RQ; ++r) read(q * RQ + r, st, 1, here1);
+            for (int r = 0; r < RQ; ++r) read(q * RQ + r, st, 1, here_a, here_b);
 #pragma unroll
             for (int r = 0; r < CQ; ++r)
                 if (q * CQ + r < OPS) {
-                    if constexpr (kStep == 0) issue(q * CQ + r, lds0 + st_fill, more);
-                    else issue_adapter(q * CQ + r, lds0 + st_fill, d);
+                    if constexpr (kStep == 0) issue(q * CQ + r, lds0 + st_fill, more, i + NS - 1);
+                    else issue_adapter(q * CQ + r, lds0 + st_fill, i + NS - 1);
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -294,8 +347,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
             mfma(std::integral_constant<int, 1>{}, q);
 #pragma unroll
             for (int r = 0; r < RQ; ++r) {
-                read(q * RQ + r, st_next, 0, next0);
-                if constexpr (kStep != 2) read_scale(q * RQ + r, st_next);
+                read(q * RQ + r, st_next, 0, next_a, next_b);
+                if constexpr (kStep != 2) read_scale(q * RQ + r, st_next, i + 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -314,7 +367,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
     QE_WG_BARRIER();  // the copies of every wave have landed
     constexpr int COLS = NB * 32, PITCH = COLS * 4 + 16;  // channels and LDS bytes of a row
     static_assert(NW * 32 * PITCH <= NS * STAGE, "the ring holds the waves' rows");
-    uint8_t* turn = smem + wid * 32 * PITCH;
+    uint8_t* flip = smem + wid * 32 * PITCH;
     const int c0 = n0 + wn * COLS;
     auto out = [&](auto kind) {
         constexpr int kOut = decltype(kind)::value;  // 0 partial sums, 1 float32, 2 bf16
@@ -327,11 +380,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
             for (int j = 0; j < 16; ++j)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-                    *reinterpret_cast<float*>(turn + acc_row(j, lane) * PITCH + (n * 32 + lr) * 4) = acc[m][n][j];
+                    *reinterpret_cast<float*>(flip + acc_row(j, lane) * PITCH + (n * 32 + lr) * 4) = acc[m][n][j];
 #pragma unroll
             for (int j = 0; j < 32 / RPI; ++j) {
                 const int r = j * RPI + lane / LPR, q = (wm * MB + m) * 32 + r;
-                const v4f* p = reinterpret_cast<const v4f*>(turn + r * PITCH + c * 4);
+                const v4f* p = reinterpret_cast<const v4f*>(flip + r * PITCH + c * 4);
                 const v4f lo = p[0];
                 if (m0 + q >= T || c0 + c >= G.d_out) continue;
                 const size_t o = (size_t)s_tok[q] * G.d_out + c0 + c;
