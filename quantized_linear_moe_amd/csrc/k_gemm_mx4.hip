@@ -409,20 +409,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
 }
 
 // ------------------------------------------------------------------ weight streaming
-// Up to 32 * TB tokens: a workgroup takes 32 channels (and a K split); its 8 waves take the 128-wide K
-// steps in turn, each loading its weight fragments (one contiguous 2 KB per step) and the token rows
+// Up to 32 * TB tokens: a workgroup takes 32 channels; its 16 waves take the 128-wide K steps in turn, each loading its weight fragments (one contiguous 2 KB per step) and the token rows
 // straight into registers, 4 steps at a time; the adapter terms are more steps, dealt to the waves
 // alike.  The waves' sums meet in LDS and are added in wave order.
-constexpr int SW = 8;  // waves
+constexpr int SW = 16;  // waves
 constexpr int SU = 4;  // K steps requested together by a wave
 
 template <int TB>
-__global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int ksplit) {
-    __shared__ float red[SW][TB * 16][64];
+__global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G) {
+    __shared__ float red[SW][16][64];
     const int tid = threadIdx.x, wid = tid >> 6, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-    const int nb = blockIdx.x, ky = blockIdx.y;
-    const int T = G.T, KB = G.d_in / 128;
-    const int kb0 = (int)((long)ky * KB / ksplit), kb1 = (int)((long)(ky + 1) * KB / ksplit);
+    const int nb = blockIdx.x, T = G.T, KB = G.d_in / 128;
 
     const v4i* w = reinterpret_cast<const v4i*>(G.w_tiled) + (size_t)nb * KB * 128 + lane;
     const uint32_t* ws = G.w_scale + (size_t)nb * KB * 32 + lr;
@@ -439,12 +436,12 @@ __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int kspl
 #pragma unroll
     for (int b = 0; b < TB; ++b) acc[b] = v16f{};
 
-    for (int kb = kb0 + wid; kb < kb1; kb += SW * SU) {
+    for (int kb = wid; kb < KB; kb += SW * SU) {
         v4i wf[SU][2], af[SU][TB][2];
         uint32_t wsc[SU], asc[SU][TB];
 #pragma unroll
         for (int s = 0; s < SU; ++s) {  // steps past the end repeat the last one and are not used
-            const int k = min(kb + s * SW, kb1 - 1);
+            const int k = min(kb + s * SW, KB - 1);
             wf[s][0] = w[(size_t)k * 128];
             wf[s][1] = w[(size_t)k * 128 + 64];
             wsc[s] = ws[(size_t)k * 32];
@@ -457,7 +454,7 @@ __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int kspl
         }
 #pragma unroll
         for (int s = 0; s < SU; ++s) {
-            if (kb + s * SW >= kb1) break;
+            if (kb + s * SW >= KB) break;
             const uint32_t sw = wsc[s] >> (8 * lh);
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
@@ -470,7 +467,7 @@ __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int kspl
 
     const int ch = min(nb * 32 + lr, G.d_out - 1);
     int turn = 0;  // adapter steps, dealt to the waves in turn
-    if (G.u && ky == 0) {
+    if (G.u) {
         for (int k = 0; k < G.rs_pad; k += 16, ++turn) {
             if (turn % SW != wid) continue;
             const v8bf b = *reinterpret_cast<const v8bf*>(G.bt_s + (size_t)ch * G.rs_pad + k + lh * 8);
@@ -481,7 +478,7 @@ __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int kspl
             }
         }
     }
-    if (G.v && ky == 0) {
+    if (G.v) {
         int ex[TB];
         uint32_t present = 0;
 #pragma unroll
@@ -506,22 +503,21 @@ __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G, int kspl
     }
 
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
+    for (int b = 0; b < TB; ++b) {
+        if (b > 0) __syncthreads();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (b * 32 + 8 * (i >> 2) < T) red[wid][b * 16 + i][lane] = acc[b][i];
-    __syncthreads();
-    float* part = ksplit > 1 ? G.part + (size_t)ky * T * G.d_out : nullptr;
-    for (int e = tid; e < TB * 16 * 64; e += 64 * SW) {
-        const int i = e >> 6, l = e & 63;
-        const int t = (i >> 4) * 32 + acc_row(i & 15, l), c = nb * 32 + (l & 31);
-        if (t >= T || c >= G.d_out) continue;
-        float s = red[0][i][l];
+            if (b * 32 + 8 * (i >> 2) < T) red[wid][i][lane] = acc[b][i];
+        __syncthreads();
+        for (int e = tid; e < 16 * 64; e += 64 * SW) {
+            const int i = e >> 6, l = e & 63;
+            const int t = b * 32 + acc_row(i, l), c = nb * 32 + (l & 31);
+            if (t >= T || c >= G.d_out) continue;
+            float s = red[0][i][l];
 #pragma unroll
-        for (int q = 1; q < SW; ++q) s += red[q][i][l];
-        const size_t o = (size_t)t * G.d_out + c;
-        if (part) part[o] = s;
-        else store_out(G.y, o, s, G.y_bf16);
+            for (int q = 1; q < SW; ++q) s += red[q][i][l];
+            store_out(G.y, (size_t)t * G.d_out + c, s, G.y_bf16);
+        }
     }
 }
 
@@ -541,19 +537,27 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(const float* __restrict
     }
 }
 
+// Which kernel.  Times are us per call with both corrections (8 experts, ranks 32), weights not in the caches.
+//   * Weight streaming re-reads the token rows for every 32 channels, about T row requests per step and CU; the
+//     weights themselves bound it up to 12 tokens.  8192 -> 29568: 8 tokens 26 streamed, 29 in 64 x 128 tiles;
+//     16 tokens 34, 31; 32 tokens 53, 36.  29568 -> 8192 (a quarter of the steps per CU): 16 tokens 28, 33;
+//     32 tokens 46, 35.  8192 -> 1024: 32 tokens 13, 15.
+//   * 256 x 256 tiles, one per CU, where they give every CU one: 1024 x 8192 -> 8192 54, 512 tokens (128 x 128) 36.
+//   * 128 x 128 tiles, two per CU: 128 x 8192 -> 29568 47, in 64 x 128 tiles 59; 512 x 8192 -> 8192 36, 40.
+//   * 64 x 128 tiles: 32 x 8192 -> 29568 36, in 128 x 128 tiles 43.  Long sums in few tiles are split:
+//     128 x 29568 -> 8192 76 unsplit, 53 in 2 or 4; 64 x 29568 -> 8192 80, 53, 41.
+//   * 64 x 64 tiles, split until there are about 512: 128 x 18944 -> 3584 40 unsplit, 23 split.
 Mx4Plan mx4_plan(int T, int d_in, int d_out) {
-    Mx4Plan P{0, 1};
-    const int KB = d_in / 128;
-    if (T <= 0) return P;
-    if (T <= kMxMaxTStream) {
-        const int wgs = (d_out + 31) / 32;
-        P.ksplit = std::max(1, std::min(512 / wgs, KB / SW));
-        return P;
-    }
-    auto tiles = [&](int b) { return (long)((T + b - 1) / b) * ((d_out + b - 1) / b); };
-    P.kind = tiles(256) >= 256 ? 256 : tiles(128) >= 192 ? 128 : 64;
-    const long n = tiles(P.kind);
-    if (n < 256) P.ksplit = (int)std::max(1l, std::min(512 / n, (long)KB / 8));
+    Mx4Plan P{0, 0, 1};
+    const int KB = d_in / 128, wgs = (d_out + 31) / 32;
+    if (T <= 12 || (T <= kMxMaxTStream && (long)((wgs + 255) / 256) * KB * T <= 3800)) return P;
+    auto tiles = [&](int bm, int bn) { return (long)((T + bm - 1) / bm) * ((d_out + bn - 1) / bn); };
+    const long t128 = tiles(64, 128), t64 = tiles(64, 64);
+    if (tiles(256, 256) >= 256 && KB >= 8) P = {256, 256, 1};
+    else if (T > 64 && tiles(128, 128) >= 192) P = {128, 128, 1};
+    else if (t128 >= 200) P = {64, 128, 1};
+    else if (t128 >= 50 && KB >= 64) P = {64, 128, (int)std::min(512 / t128, 4l)};
+    else P = {64, 64, (int)std::max(1l, std::min(512 / std::min(t64, 512l), (long)KB / 8))};
     return P;
 }
 
@@ -567,35 +571,39 @@ static int mx4_main_columns(int n_tm, int n_tn) {
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
     if (G.T <= 0) return hipSuccess;
-    if (P.kind == 0) {
-        const dim3 grid((G.d_out + 31) / 32, P.ksplit), block(64 * SW);
-        if (G.T <= 32) hipLaunchKernelGGL(stream_mx4_kernel<1>, grid, block, 0, st, G, P.ksplit);
-        else hipLaunchKernelGGL(stream_mx4_kernel<2>, grid, block, 0, st, G, P.ksplit);
-    } else {
-        Mx4Gemm H = G;
-        if (P.kind == 256) {
-            const hipError_t e = launch_mx4_prep(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
-            if (e != hipSuccess) return e;
-            H.codes = G.a_tiled;
-            H.scales = reinterpret_cast<const uint8_t*>(G.a_scale);
-            const int n_tm = (G.T + 255) / 256, n_tn = mx4_main_columns(n_tm, (G.d_out + 255) / 256);
-            hipLaunchKernelGGL((gemm_mx4_kernel<256, 256, 2, 4, true, 4>), dim3((unsigned)((size_t)n_tm * n_tn), P.ksplit),
-                               dim3(512), 0, st, H, n_tm, 0, P.ksplit);
-            if (n_tn * 256 < G.d_out) {
-                const int r_tm = (G.T + 127) / 128, r_tn = (G.d_out - n_tn * 256 + 127) / 128;
-                hipLaunchKernelGGL((gemm_mx4_kernel<128, 128, 2, 2, true, 4>), dim3((unsigned)((size_t)r_tm * r_tn), P.ksplit),
-                                   dim3(256), 0, st, H, r_tm, n_tn * 256, P.ksplit);
-            }
-        } else {
-            const int n_tm = (G.T + P.kind - 1) / P.kind, n_tn = (G.d_out + P.kind - 1) / P.kind;
-            const dim3 grid((unsigned)((size_t)n_tm * n_tn), P.ksplit);
-            if (P.kind == 128)
-                hipLaunchKernelGGL((gemm_mx4_kernel<128, 128, 2, 2, false, 4>), grid, dim3(256), 0, st, H, n_tm, 0, P.ksplit);
-            else
-                hipLaunchKernelGGL((gemm_mx4_kernel<64, 64, 2, 2, false, 4>), grid, dim3(256), 0, st, H, n_tm, 0, P.ksplit);
-        }
+    if (P.bm == 0) {
+        const dim3 grid((G.d_out + 31) / 32), block(64 * SW);
+        if (G.T <= 32) hipLaunchKernelGGL(stream_mx4_kernel<1>, grid, block, 0, st, G);
+        else hipLaunchKernelGGL(stream_mx4_kernel<2>, grid, block, 0, st, G);
+        return hipGetLastError();
     }
-    hipError_t e = hipGetLastError();
+    Mx4Gemm H = G;
+    if (P.bm == 256) {
+        const hipError_t e = launch_mx4_prep(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
+        if (e != hipSuccess) return e;
+        H.codes = G.a_tiled;
+        H.scales = reinterpret_cast<const uint8_t*>(G.a_scale);
+    }
+    // one launch: tiles of channels n_off, n_off + bn, ... (columns of them) by all tokens
+    auto launch = [&](auto kernel, int bm, int bn, int threads, int n_off, int columns) {
+        const int n_tm = (G.T + bm - 1) / bm;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((size_t)n_tm * columns), P.ksplit), dim3(threads), 0, st, H, n_tm,
+                           n_off, P.ksplit);
+    };
+    const int columns = (G.d_out + P.bn - 1) / P.bn;
+    if (P.bm == 256) {
+        const int main = mx4_main_columns((G.T + 255) / 256, columns);
+        launch(gemm_mx4_kernel<256, 256, 2, 4, true, 4>, 256, 256, 512, 0, main);
+        if (main * 256 < G.d_out)
+            launch(gemm_mx4_kernel<128, 128, 2, 2, true, 4>, 128, 128, 256, main * 256, (G.d_out - main * 256 + 127) / 128);
+    } else if (P.bm == 128) {
+        launch(gemm_mx4_kernel<128, 128, 2, 2, false, 4>, 128, 128, 256, 0, columns);
+    } else if (P.bn == 128) {
+        launch(gemm_mx4_kernel<64, 128, 2, 2, false, 4>, 64, 128, 256, 0, columns);
+    } else {
+        launch(gemm_mx4_kernel<64, 64, 2, 2, false, 4>, 64, 64, 256, 0, columns);
+    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || P.ksplit == 1) return e;
     const size_t n = (size_t)G.T * G.d_out;
     hipLaunchKernelGGL(mx4_finish_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, G.part, P.ksplit, n,

@@ -221,7 +221,7 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     const int skinny_parts = mx4(lin) && W.skinny_ksplit == 1 ? 0 : W.skinny_ksplit;
     off = align256(off + (size_t)std::max({skinny_parts, D.ks_m, W.gemm_ksplit > 1 ? W.gemm_ksplit : 0}) * t *
                              lin->d_out * 4);
-    const bool tiles = mx4(lin) && mx4_plan(T, lin->d_in, lin->d_out).kind == 256;
+    const bool tiles = mx4(lin) && mx4_plan(T, lin->d_in, lin->d_out).bm == 256;
     W.a_tiled = off;
     off = align256(off + (tiles ? mx4_tile_codes(t, lin->d_in) : 0));
     W.a_scale = off;
@@ -796,7 +796,7 @@ int qe_linear_forward(const qe_linear* lin, const void* x, int32_t x_dtype, int3
         // both corrections; tiles of many tokens walk them in expert order
         st = run_xpass(lin, x, x_dtype, T, u != nullptr, route, route, nullptr, nullptr, expert, u, v, ws, s);
         if (st) return st;
-        int32_t* perm = route && mx4_plan(T, lin->d_in, lin->d_out).kind != 0 ? at<int32_t>(ws, W.perm) : nullptr;
+        int32_t* perm = route && mx4_plan(T, lin->d_in, lin->d_out).bm != 0 ? at<int32_t>(ws, W.perm) : nullptr;
         if (perm)
             QE_TRY_HIP(launch_bucket(expert, T, lin->n_routed, at<int32_t>(ws, W.counts), at<int32_t>(ws, W.offsets),
                                      perm, s));

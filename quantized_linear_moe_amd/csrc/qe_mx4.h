@@ -82,7 +82,7 @@ inline size_t mx4_tile_scales(size_t rows, size_t d_in) { return (rows + 31) / 3
 // How the product runs for T tokens: which kernel and how many K splits (more than one: float32
 // partials [ksplit][T][d_out] in the workspace, added by a finish kernel)
 struct Mx4Plan {
-    int kind;    // 0: weight streaming (T <= kMxMaxTStream); else the tile's tokens (and channels)
+    int bm, bn;  // tokens and channels of a tile; 0: weight streaming (T <= kMxMaxTStream)
     int ksplit;
 };
 Mx4Plan mx4_plan(int T, int d_in, int d_out);

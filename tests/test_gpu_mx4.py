@@ -181,7 +181,8 @@ SHAPES = [  # T, d_in, d_out, r_s, n_r, r_r
     (16, 1152, 2064, 0, 16, 64), (32, 640, 400, 64, 0, 0), (33, 1024, 96, 8, 3, 48), (64, 896, 528, 33, 2, 1),
     (65, 128, 16, 0, 0, 0), (65, 2048, 272, 32, 8, 32), (127, 1280, 304, 0, 4, 16), (128, 512, 2064, 16, 8, 8),
     (200, 256, 1040, 64, 16, 64), (513, 1536, 256, 8, 4, 48), (1000, 640, 1552, 32, 8, 32), (2048, 256, 8208, 32, 8, 32),
-    (4099, 128, 4112, 8, 4, 8),
+    (4099, 128, 4112, 8, 4, 8), (40, 512, 25616, 32, 8, 32), (100, 8192, 3216, 32, 8, 32), (17, 8192, 528, 16, 4, 64),
+    (257, 1152, 16400, 8, 16, 32), (4352, 1024, 4112, 32, 8, 32), (48, 1024, 4112, 64, 16, 64),
 ]
 
 
