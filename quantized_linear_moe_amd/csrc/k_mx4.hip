@@ -33,27 +33,15 @@ __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if constexpr (kSmooth == 1) is[i] = 1.0f / s[i];
-            s_ok = s_ok && s[i] >= 0x1p-90f && s[i] <= 0x1p90f;
         }
+        s_ok = code_div_ok(s);
     }
     const long t0 = (long)blockIdx.y * rows, t1 = min((long)T, t0 + rows);
     for (long t = t0 + rr; t < t1; t += step) {
         float v[8];
         load8(x, kBf16 ? QE_BF16 : QE_F32, (size_t)t * d + j, v);
         if constexpr (kSmooth == 1) {
-            bool ok = s_ok;
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q[i] = div_markstein(v[i], s[i], is[i]);
-                ok = ok && in_markstein_range(v[i]);
-            }
-            if (__builtin_expect(__any(!ok), 0)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q[i] = v[i] / s[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = q[i];
+            code_div8(v, s, is, s_ok);
         } else if constexpr (kSmooth == 2) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= s[i];

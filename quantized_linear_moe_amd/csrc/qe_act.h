@@ -85,18 +85,60 @@ __device__ inline void smooth8(const float* __restrict__ smooth, const float* __
     for (int i = 0; i < 8; ++i) v[i] = r[i];
 }
 
-// 8 per-token integer codes clamp(rint(v / sx), -fq, fq) (sx == 0: zeros), packed
-__device__ inline v2u quant8(const float v[8], float sx, float fq) {
-    const float inv = sx != 0.0f ? 1.0f / sx : 0.0f;
-    const bool fast = sx >= 0x1p-90f && sx <= 0x1p90f;
-    uint32_t packed[2] = {0u, 0u};
+// largest |v| of 8 values (NaN: ignored)
+__device__ inline float absmax8(const float v[8]) {
+    float m = __builtin_fabsf(v[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = fast ? div_markstein(v[i], sx, inv) : v[i] / sx;
-        const float c = sx != 0.0f ? fminf(fmaxf(__builtin_rintf(q), -fq), fq) : 0.0f;
-        packed[i >> 2] |= ((uint32_t)(int32_t)c & 0xFFu) << (8 * (i & 3));
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, __builtin_fabsf(v[i]));
+    return m;
+}
+
+// v / s for 8 channels whose factors' reciprocals are kept, as codes need it: exactly the IEEE quotient,
+// except that a quotient too small to get a code other than zero may be off.  One range check serves the 8
+// values: with all s in [2^-20, 2^20] (s_ok) and their largest |v| in [2^-40, 2^100], the corrected quotient
+// is exact for |v| >= 2^-100, and a smaller |v| gives less than 2^-80 beside a largest quotient of at
+// least 2^-60, far below half a code.  Otherwise the division itself.
+__device__ inline void code_div8(float v[8], const float s[8], const float is[8], bool s_ok) {
+    const float m = absmax8(v);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = div_markstein(v[i], s[i], is[i]);
+    if (__builtin_expect(__any(!(s_ok && (m == 0.0f || (m >= 0x1p-40f && m <= 0x1p100f)))), 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = v[i] / s[i];
     }
-    return v2u{packed[0], packed[1]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = q[i];
+}
+__device__ inline bool code_div_ok(const float s[8]) {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ok = ok && s[i] >= 0x1p-20f && s[i] <= 0x1p20f;
+    return ok;
+}
+
+// 8 per-token integer codes rint(v / sx) (sx == 0: zeros), packed, for |v| <= amax and sx = amax / qmax:
+// the quotient is at most qmax (1 + 2^-23), so no code exceeds qmax.  Adding 1.5 * 2^23 rounds to the nearest
+// even integer, whose two's complement low byte is then the sum's.
+__device__ inline v2u quant8(const float v[8], float sx) {
+    const float inv = sx != 0.0f ? 1.0f / sx : 0.0f;
+    const bool fast = sx >= 0x1p-90f && sx <= 0x1p90f;  // (the same in the whole row)
+    uint32_t b[8];
+    if (fast) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(div_markstein(v[i], sx, inv) + 12582912.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = sx != 0.0f ? __float_as_uint(v[i] / sx + 12582912.0f) : 0u;
+    }
+    v2u out;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * k + 1], b[4 * k], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * k + 3], b[4 * k + 2], 0x04000C0Cu);
+        out[k] = lo | hi;
+    }
+    return out;
 }
 
 }  // namespace qe
