@@ -58,9 +58,16 @@ __device__ inline void store_out(float* y, size_t idx, float v, bool y_bf16) {
 // Operands that come as rows (adapters; activations unless TA) are copied 16 rows of 64 bytes at a time,
 // a row's four chunks of 16 stored at chunk ^ ((row >> 2) & 3), so that the fragment reads of 16
 // neighbouring rows reach all 64 banks.  TA: the activations come as tiles like the weights
-// (mx4_prep_kernel, in the order of perm), every copy contiguous.  Otherwise their scales, one dword per row
+// (mx4_tile_kernel, in the order of perm), every copy contiguous.  Otherwise their scales, one dword per row
 // and step, are copied four steps at a time, 16 rows per copy, into four slots of their own: step by step
 // every row's dword would be a memory request of its own, as many as the codes make.
+//
+// What bounds the large tile, 4096 x 8192 -> 29568 without corrections, in a long loop (us; 1.98e12
+// operations): 498 in 4 x 2 waves (64 x 128 channels each), 505 in 2 x 4, 508 in 2 x 2 of 128 x 128; without
+// the stores of y 451, without the copies' traffic 450, without both 429; the same products on registers
+// alone 300 (6.6 POP/s: the clock falls with the power that they draw).  Tiles in turn in resident
+// workgroups, the next one's first copies behind the stores of the last, took out the stalls between tiles
+// but no time.  With both corrections 535, into bf16 500.
 template <int BM, int BN, int WM, int WN, bool TA, int NS>
 __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, int n_tm, int n_off, int ksplit) {
     constexpr int NW = WM * WN;
@@ -409,11 +416,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gemm_mx4_kernel(Mx4Gemm G, in
 }
 
 // ------------------------------------------------------------------ weight streaming
-// Up to 32 * TB tokens: a workgroup takes 32 channels; its 16 waves take the 128-wide K steps in turn, each loading its weight fragments (one contiguous 2 KB per step) and the token rows
-// straight into registers, 4 steps at a time; the adapter terms are more steps, dealt to the waves
-// alike.  The waves' sums meet in LDS and are added in wave order.
+// Up to 32 * TB tokens: a workgroup takes 32 channels; its waves take the 128-wide K steps in turn, each
+// loading its weight fragments (one contiguous 2 KB per step) and the token rows straight into registers,
+// SU steps at a time; the adapter terms are more steps, dealt to the waves alike.  The waves' sums meet in
+// LDS and are added in wave order.
 constexpr int SW = 16;  // waves
-constexpr int SU = 4;  // K steps requested together by a wave
+constexpr int SU = 4;   // K steps requested together by a wave
 
 template <int TB>
 __global__ __launch_bounds__(64 * SW) void stream_mx4_kernel(Mx4Gemm G) {
@@ -579,7 +587,7 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
     }
     Mx4Gemm H = G;
     if (P.bm == 256) {
-        const hipError_t e = launch_mx4_prep(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
+        const hipError_t e = launch_mx4_tile(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
         if (e != hipSuccess) return e;
         H.codes = G.a_tiled;
         H.scales = reinterpret_cast<const uint8_t*>(G.a_scale);
@@ -593,7 +601,7 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
     const int columns = (G.d_out + P.bn - 1) / P.bn;
     if (P.bm == 256) {
         const int main = mx4_main_columns((G.T + 255) / 256, columns);
-        launch(gemm_mx4_kernel<256, 256, 2, 4, true, 4>, 256, 256, 512, 0, main);
+        launch(gemm_mx4_kernel<256, 256, 4, 2, true, 4>, 256, 256, 512, 0, main);
         if (main * 256 < G.d_out)
             launch(gemm_mx4_kernel<128, 128, 2, 2, true, 4>, 128, 128, 256, main * 256, (G.d_out - main * 256 + 127) / 128);
     } else if (P.bm == 128) {

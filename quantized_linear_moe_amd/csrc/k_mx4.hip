@@ -134,32 +134,40 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T
 // one operand fragment of the 32x32x64 product and exactly one scale block.  Scales: one dword per
 // channel and K step, byte i the scale of its block i, ordered (channel block, K step, channel).
 // Channels past d_out (an odd number of 16-channel groups) hold zeros.
-__global__ __launch_bounds__(256) void mx4_prep_kernel(const uint8_t* __restrict__ codes,
+//
+// The same layout holds a product's activations (rows: tokens, in the order of perm when it is given).  A wave
+// reads two steps of 32 rows, 64 bytes per row and step, and writes them as 512-byte pieces.
+__global__ __launch_bounds__(256) void mx4_tile_kernel(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales,
                                                        const int32_t* __restrict__ perm, int rows, int d_in,
                                                        v4u* __restrict__ tiled, uint32_t* __restrict__ tiled_scale) {
     const int KB = d_in / 128, NB = (rows + 31) / 32;
-    const size_t n = (size_t)NB * KB * 128, stride = (size_t)gridDim.x * 256;
+    const size_t n = (size_t)NB * KB * 32, stride = (size_t)gridDim.x * 256;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
-        const int l = (int)(i & 63), h = (int)(i >> 6) & 1;
-        const size_t q = i >> 7;
+        const int l = (int)(i & 31);
+        const size_t q = i >> 5;  // (row block, K step)
         const int nb = (int)(q / KB), kb = (int)(q - (size_t)nb * KB);
-        const int pos = nb * 32 + (l & 31);
-        const size_t r = pos >= rows ? 0 : perm ? perm[pos] : pos;
-        v4u c = v4u{0, 0, 0, 0};
-        if (pos < rows) c = *reinterpret_cast<const v4u*>(codes + r * (d_in / 2) + kb * 64 + h * 32 + (l >> 5) * 16);
-        tiled[i] = c;
-        if (h == 0 && l < 32)
-            tiled_scale[q * 32 + l] =
-                pos < rows ? *reinterpret_cast<const uint32_t*>(scales + r * (d_in / 32) + kb * 4) : 0u;
+        const int pos = nb * 32 + l;
+        v4u c[4] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
+        uint32_t sc = 0;
+        if (pos < rows) {
+            const size_t r = perm ? perm[pos] : pos;
+            const v4u* p = reinterpret_cast<const v4u*>(codes + r * (d_in / 2) + (size_t)kb * 64);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = p[k];
+            sc = *reinterpret_cast<const uint32_t*>(scales + r * (d_in / 32) + kb * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tiled[q * 128 + k * 32 + l] = c[k];  // chunk k: half step k / 2, lanes 32 (k % 2) + l
+        tiled_scale[q * 32 + l] = sc;
     }
 }
 
-hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
+hipError_t launch_mx4_tile(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
                            uint8_t* tiled, uint32_t* tiled_scale, hipStream_t st) {
-    const size_t n = (size_t)((rows + 31) / 32) * (d_in / 128) * 128;
-    const unsigned grid = (unsigned)std::min<size_t>((n + 255) / 256, 256 * 32);
-    hipLaunchKernelGGL(mx4_prep_kernel, dim3(grid), dim3(256), 0, st, codes, scales, perm, rows, d_in,
+    const size_t n = (size_t)((rows + 31) / 32) * (d_in / 128) * 32;
+    const unsigned grid = (unsigned)std::min<size_t>((n + 255) / 256, 256 * 16);
+    hipLaunchKernelGGL(mx4_tile_kernel, dim3(grid), dim3(256), 0, st, codes, scales, perm, rows, d_in,
                        reinterpret_cast<v4u*>(tiled), tiled_scale);
     return hipGetLastError();
 }

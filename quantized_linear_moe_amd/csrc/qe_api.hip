@@ -415,7 +415,7 @@ int qe_mx4_prepare(const qe_linear* lin, const uint8_t* w_codes, const uint8_t* 
         QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
     const PrepLayout L = prep_layout(lin);
     hipStream_t s = S(stream);
-    QE_TRY_HIP(launch_mx4_prep(w_codes, w_scales, nullptr, lin->d_out, lin->d_in, at<uint8_t>(prep, L.w_tiled),
+    QE_TRY_HIP(launch_mx4_tile(w_codes, w_scales, nullptr, lin->d_out, lin->d_in, at<uint8_t>(prep, L.w_tiled),
                                at<uint32_t>(prep, L.w_scale), s));
     return prepare_rest(lin, smooth, A_s, B_s, A_r, B_r, R, prep, s);
 }

@@ -73,7 +73,7 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T
                               hipStream_t st);
 // canonical codes and scales of [rows][d_in] into the product's tiles (see k_mx4.hip), rows in the
 // order of `perm` when it is given
-hipError_t launch_mx4_prep(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
+hipError_t launch_mx4_tile(const uint8_t* codes, const uint8_t* scales, const int32_t* perm, int rows, int d_in,
                            uint8_t* tiled, uint32_t* tiled_scale, hipStream_t st);
 // bytes of the tiles of [rows][d_in] (codes, scales)
 inline size_t mx4_tile_codes(size_t rows, size_t d_in) { return (rows + 31) / 32 * 32 * d_in / 2; }
