@@ -573,8 +573,9 @@ Mx4Plan mx4_plan(int T, int d_in, int d_out) {
 // few of the 256 CUs is given to 128 x 128 tiles instead (two per CU, a quarter of the work each).
 static int mx4_main_columns(int n_tm, int n_tn) {
     const long n = (long)n_tm * n_tn, rounds = n / 256, rest = n - rounds * 256;
-    if (rounds == 0 || rest == 0 || rest > 96) return n_tn;
-    return (int)(rounds * 256 / n_tm);
+    const int main = (int)(rounds * 256 / n_tm);
+    // (main 0: a column has more tiles than the full rounds)
+    return rest == 0 || rest > 96 || main == 0 ? n_tn : main;
 }
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {

@@ -385,3 +385,74 @@ def test_top2_forward(Q):
     slack = np.stack([vm[t] @ np.abs(B[e2[t]]) for t in range(T)])
     tol = 2.0 ** -8 * mag + 300 * 2.0 ** -23 * (slack + np.abs(y2.double().cpu().numpy()))
     assert np.all(np.abs(got - term) <= tol)
+
+
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_group_of_mixed_linears(Q, T):
+    """A group forward is its linears' own forwards, whatever their settings."""
+    L = Q.libqe
+    cfg = synth.get_config("qwen2vl_2b")
+    specs = {l.name: l for l in cfg.linears}
+    x = synth.gen_activations(cfg, specs["q"].stream, T=T).to(DEV)
+    layers = [Q.QELinear.from_params(synth.gen_linear(cfg, specs[n]), 4, a, device=DEV)
+              for n, a in (("q", 4), ("k", 8), ("v", 4))]
+    own_e = [torch.full((T,), -1, dtype=torch.int32, device=DEV) for _ in layers]
+    own = [l.forward(x, expert_out=e) for l, e in zip(layers, own_e)]
+    for pick in ([0, 1, 2], [0, 2], [2]):
+        y = [torch.empty_like(own[i]) for i in pick]
+        e = [torch.empty_like(own_e[i]) for i in pick]
+        L.qe_group_forward([layers[i].lin for i in pick], x, y, e, [layers[i].workspace(T) for i in pick])
+        for i, a, b in zip(pick, y, e):
+            assert torch.equal(a, own[i]) and torch.equal(b, own_e[i])
+
+
+@pytest.mark.parametrize("T", [9, 300])
+def test_routed_term_added_apart(Q, T):
+    """qe_mx4_gemm without the routed term, then qe_routed_lora, which adds (bf16(x) . A_e) . B_e: v is rounded to
+    bf16 in both ways from float32 sums that may differ, so |dy| <= 2^-7 |v| |B_e| plus float32 rounding."""
+    L = Q.libqe
+    cfg = synth.get_config("qwen2vl_2b")
+    spec = next(l for l in cfg.linears if l.name == "k")
+    params = synth.gen_linear(cfg, spec)
+    layer = Q.QELinear.from_params(params, 4, 4, device=DEV)
+    x = synth.gen_activations(cfg, spec.stream, T=T).to(DEV)
+    ws = layer.workspace(T)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    e, counts, offsets, perm = i32(T), i32(cfg.n_routed), i32(cfg.n_routed + 1), i32(T)
+    L.qe_route(layer.lin, x, None, e, counts, offsets, perm, ws)
+    u = torch.empty(T, L.rank_pad(cfg.r_shared), dtype=torch.bfloat16, device=DEV)
+    v = torch.empty(T, L.rank_pad(cfg.r_routed), dtype=torch.bfloat16, device=DEV)
+    L.qe_adapter_inputs(layer.lin, x, e, u, v, ws)
+    codes = torch.empty(T, spec.d_in // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(T, spec.d_in // 32, dtype=torch.uint8, device=DEV)
+    L.qe_mx4_quant(x, _dev(params["s"]), codes, scales)
+    y = [torch.empty(T, spec.d_out, dtype=torch.float32, device=DEV) for _ in range(2)]
+    L.qe_mx4_gemm(layer.lin, codes, scales, u, v, e, y[0], ws)
+    L.qe_mx4_gemm(layer.lin, codes, scales, u, None, None, y[1], ws)
+    L.qe_routed_lora(layer.lin, x, e, offsets, perm, y[1], ws)
+    a, w = (M.mx4_values(M.unpack(c.cpu().numpy()), t.cpu().numpy())
+            for c, t in ((codes, scales), (layer.packed, layer.w_scale)))
+    B_s, B_r, u, v, e = (t.double().cpu().numpy() for t in (params["B_s"], params["B_r"], u, v, e))
+    u, v, e = u[:, :cfg.r_shared], v[:, :cfg.r_routed], e.astype(np.int32)
+    _, mag = M.mx4_gemm(a, w, u, B_s, v, e, B_r)
+    _, routed = M.mx4_gemm(a * 0, w, None, None, v, e, B_r)
+    tol = 2.0 ** -7 * routed + 2 * (spec.d_in + 64) * 2.0 ** -23 * mag
+    assert np.all(np.abs((y[0].double() - y[1].double()).cpu().numpy()) <= tol)
+
+
+def test_no_tokens(Q):
+    """Calls without tokens return at once and leave everything as it was."""
+    L = Q.libqe
+    rng = np.random.default_rng(2)
+    layer = Q.QELinear.from_params(dict(W_f=rng.standard_normal((48, 256)).astype(np.float32)), 4, 4, device=DEV)
+    u8 = lambda n: torch.empty(0, n, dtype=torch.uint8, device=DEV)  # noqa: E731
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(256, device=DEV)
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    y = torch.empty(0, 48, device=DEV)
+    L.qe_mx4_quant(x, w, u8(128), u8(8))
+    L.qe_mx4_dequant(u8(128), u8(8), x)
+    L.qe_mx4_gemm(layer.lin, u8(128), u8(8), None, None, None, y, ws)
+    L.qe_add_rmsnorm(x, x, w, 1e-6, h=x.clone(), xn=x.clone(), a_bits=4, codes=u8(128), scales=u8(8))
+    L.qe_linear_forward(layer.lin, x, y, None, ws)
+    torch.cuda.synchronize()
