@@ -73,7 +73,8 @@ typedef enum { QE_F32 = 0, QE_BF16 = 1 } qe_dtype;
  *                qe_routed_lora and qe_linear_forward_top2 add into y and take QE_F32 only.
  *   prep         device buffer written by qe_prepare() (qe_prepared_bytes() bytes)
  * Kernel-path constraints: d_out % 16 == 0 and d_in % 128 == 0, and d_in <= 32768 when
- * a_bits is 6 or 8 (else QE_ERR_UNSUPPORTED).
+ * a_bits is 6 or 8; with a_bits 4, d_out and the tokens of a call are at most 2^30 (else
+ * QE_ERR_UNSUPPORTED, and 0 from the sizing calls).
  */
 typedef struct qe_linear {
     int32_t d_in;

@@ -557,9 +557,9 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(const float* __restrict
 //   * 64 x 64 tiles, split until there are about 512: 128 x 18944 -> 3584 40 unsplit, 23 split.
 Mx4Plan mx4_plan(int T, int d_in, int d_out) {
     Mx4Plan P{0, 0, 1};
-    const int KB = d_in / 128, wgs = (d_out + 31) / 32;
+    const int KB = d_in / 128, wgs = (int)(((long)d_out + 31) / 32);
     if (T <= 12 || (T <= kMxMaxTStream && (long)((wgs + 255) / 256) * KB * T <= 3800)) return P;
-    auto tiles = [&](int bm, int bn) { return (long)((T + bm - 1) / bm) * ((d_out + bn - 1) / bn); };
+    auto tiles = [&](int bm, int bn) { return ((long)T + bm - 1) / bm * (((long)d_out + bn - 1) / bn); };
     const long t128 = tiles(64, 128), t64 = tiles(64, 64);
     if (tiles(256, 256) >= 256 && KB >= 8) P = {256, 256, 1};
     else if (T > 64 && tiles(128, 128) >= 192) P = {128, 128, 1};

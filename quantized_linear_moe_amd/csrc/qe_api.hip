@@ -76,6 +76,7 @@ int validate_linear(const qe_linear* lin) {
     // 16 * |acc| must stay below 2^31 on the int8 path: 16 * 127 * 7 * d_in
     QE_CHECK(!int_codes(lin) || (int64_t)lin->d_in * 16 * 127 * 7 < (int64_t)INT32_MAX, QE_ERR_UNSUPPORTED);
     QE_CHECK(!int_codes(lin) || lin->d_in <= 32768, QE_ERR_UNSUPPORTED);  // one token row per workgroup
+    QE_CHECK(!mx4(lin) || lin->d_out <= kMxMaxRows, QE_ERR_UNSUPPORTED);
     return QE_OK;
 }
 
@@ -84,6 +85,7 @@ int validate_forward_common(const qe_linear* lin, int32_t T, int32_t x_dtype, co
     int st = validate_linear(lin);
     if (st) return st;
     QE_CHECK(T >= 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(!mx4(lin) || T <= kMxMaxRows, QE_ERR_UNSUPPORTED);
     QE_CHECK(x_dtype == QE_F32 || x_dtype == QE_BF16, QE_ERR_INVALID_ARG);
     QE_CHECK(lin->prep != nullptr, QE_ERR_INVALID_ARG);
     QE_CHECK(aligned16(lin->prep), QE_ERR_ALIGNMENT);
@@ -421,7 +423,7 @@ int qe_mx4_prepare(const qe_linear* lin, const uint8_t* w_codes, const uint8_t* 
 }
 
 size_t qe_workspace_bytes(const qe_linear* lin, int32_t T) {
-    if (validate_linear(lin) != QE_OK || T < 0) return 0;
+    if (validate_linear(lin) != QE_OK || T < 0 || (mx4(lin) && T > kMxMaxRows)) return 0;
     return ws_layout(lin, T).total;
 }
 

@@ -9,8 +9,9 @@ namespace qe {
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-constexpr int kMxBlock = 32;       // elements that share a scale
-constexpr int kMxMaxTStream = 64;  // token counts served by the weight-streaming product
+constexpr int kMxBlock = 32;         // elements that share a scale
+constexpr int kMxMaxRows = 1 << 30;  // tokens and output channels of a product: tile ends stay below 2^31
+constexpr int kMxMaxTStream = 64;    // token counts served by the weight-streaming product
 
 // float32 -> bf16 bits, round to nearest even, NaN kept
 __device__ inline uint32_t mx4_bf16_bits(float f) {

@@ -142,6 +142,22 @@ def test_sizes_of_microscaled_linears(L, d_in, d_out):
     assert byts == 8 * d_in * 2 + d_in * d_out * 17 / 32 + d_in * 4 + 8 * d_out * 4
 
 
+def test_sizes_past_the_tiles_are_refused(L):
+    """Tile ends are 32-bit numbers: 2^30 tokens or channels are the most that a microscaled linear takes."""
+    lib = L.raw_library()
+    lin, ref = _lin(L, r_shared=0, n_routed=0, r_routed=0), ctypes.byref
+    assert lib.qe_workspace_bytes(ref(lin), 2 ** 30) > 2 ** 30
+    for T in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert lib.qe_workspace_bytes(ref(lin), T) == 0
+        big = 2 ** 62
+        assert lib.qe_mx4_gemm(ref(lin), P, P, T, None, None, None, None, P, P, big, None) == L.QE_ERR_UNSUPPORTED
+        assert lib.qe_linear_forward(ref(lin), P, 1, T, P, None, P, big, None) == L.QE_ERR_UNSUPPORTED
+        assert lib.qe_linear_forward_noalloc(ref(lin), P, 1, T, P, None, None) == L.QE_ERR_WORKSPACE
+    wide = _lin(L, d_out=2 ** 30 + 16, r_shared=0, n_routed=0, r_routed=0)
+    assert lib.qe_prepared_bytes(ref(wide)) == 0
+    assert lib.qe_mx4_prepare(ref(wide), P, P, None, None, None, None, None, None, P, None) == L.QE_ERR_UNSUPPORTED
+
+
 def test_bindings_refuse_before_the_library_is_called(L):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     codes, scales = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
