@@ -15,6 +15,7 @@
 #include "qe_act.h"
 #include "qe_dma.h"
 #include "qe_internal.h"
+#include "qe_mx4.h"
 #include "qe_splits.h"
 
 namespace qe {
@@ -251,13 +252,12 @@ hipError_t launch_xproj(const void* x, int x_dtype, int T, int d_in, const uint1
 // One workgroup per token: each thread reduces columns of the split-K partials in a
 // fixed order, the router takes the argmin over its columns (lowest index on ties),
 // and the bf16 adapter inputs of the shared and of the selected routed expert are written.
-__global__ __launch_bounds__(1024) void xproj_finish_kernel(const float* __restrict__ part, int ksplit, int T,
-                                                            int ncols_pad, int se_col, int r_s, int rs_pad, int re_col,
-                                                            int n_r, int r_r, int rr_pad, int router_col,
-                                                            const int32_t* __restrict__ expert_in,
-                                                            float* __restrict__ scores, int32_t* __restrict__ expert_out,
-                                                            uint16_t* __restrict__ u, uint16_t* __restrict__ v,
-                                                            int32_t* __restrict__ expert2_out) {
+__device__ __forceinline__ void xproj_finish_token(const float* __restrict__ part, int ksplit, int T, int ncols_pad,
+                                                   int se_col, int r_s, int rs_pad, int re_col, int n_r, int r_r,
+                                                   int rr_pad, int router_col, const int32_t* __restrict__ expert_in,
+                                                   float* __restrict__ scores, int32_t* __restrict__ expert_out,
+                                                   uint16_t* __restrict__ u, uint16_t* __restrict__ v,
+                                                   int32_t* __restrict__ expert2_out) {
     extern __shared__ float sums[];  // [nq][ncols_pad]: partial sums over split ranges, then the total in row 0
     __shared__ int s_e;
     const int t = blockIdx.x;
@@ -339,6 +339,55 @@ __global__ __launch_bounds__(1024) void xproj_finish_kernel(const float* __restr
         for (int c = threadIdx.x; c < rr_pad; c += blockDim.x)
             v[(size_t)t * rr_pad + c] = c < r_r ? (uint16_t)f32_to_bf16_bits(sums[re_col + e * rr_pad + c]) : (uint16_t)0;
     }
+}
+
+__global__ __launch_bounds__(1024) void xproj_finish_kernel(const float* __restrict__ part, int ksplit, int T,
+                                                            int ncols_pad, int se_col, int r_s, int rs_pad, int re_col,
+                                                            int n_r, int r_r, int rr_pad, int router_col,
+                                                            const int32_t* __restrict__ expert_in,
+                                                            float* __restrict__ scores, int32_t* __restrict__ expert_out,
+                                                            uint16_t* __restrict__ u, uint16_t* __restrict__ v,
+                                                            int32_t* __restrict__ expert2_out) {
+    xproj_finish_token(part, ksplit, T, ncols_pad, se_col, r_s, rs_pad, re_col, n_r, r_r, rr_pad, router_col, expert_in,
+                       scores, expert_out, u, v, expert2_out);
+}
+
+// The same, with the microscaled codes of the tokens in the workgroups past the tokens' (XM_ROW channels
+// each): for few tokens a launch costs more than either.
+constexpr int XM_ROW = 1024 * 8;
+__global__ __launch_bounds__(1024) void xproj_finish_mx4_kernel(
+    const float* __restrict__ part, int ksplit, int T, int ncols_pad, int se_col, int r_s, int rs_pad, int re_col, int n_r,
+    int r_r, int rr_pad, int router_col, int32_t* __restrict__ expert, uint16_t* __restrict__ u, uint16_t* __restrict__ v,
+    const void* __restrict__ x, int x_dtype, int d_in, const float* __restrict__ smooth,
+    const float* __restrict__ inv_smooth, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    if (blockIdx.x < (unsigned)T) {
+        xproj_finish_token(part, ksplit, T, ncols_pad, se_col, r_s, rs_pad, re_col, n_r, r_r, rr_pad, router_col, nullptr,
+                           nullptr, expert, u, v, nullptr);
+        return;
+    }
+    const int segs = (d_in + XM_ROW - 1) / XM_ROW, b = blockIdx.x - T, t = b / segs;
+    const int j = (b - t * segs) * XM_ROW + threadIdx.x * 8;
+    if (j >= d_in) return;
+    float xv[8], s[8], is[8];
+    load8(x, x_dtype, (size_t)t * d_in + j, xv);
+    load8(smooth, QE_F32, j, s);
+    load8(inv_smooth, QE_F32, j, is);
+    code_div8(xv, s, is, code_div_ok(s));
+    mx4_store8(xv, codes + (size_t)t * (d_in / 2), scales + (size_t)t * (d_in / kMxBlock), j);
+}
+
+hipError_t launch_xproj_finish_mx4(const float* part, int ksplit, int T, int ncols_pad, int col0, int se_col, int r_s,
+                                   int rs_pad, int re_col, int n_r, int r_r, int rr_pad, int router_col,
+                                   int32_t* expert, uint16_t* u, uint16_t* v, const void* x, int x_dtype, int d_in,
+                                   const float* smooth, const float* inv_smooth, uint8_t* codes, uint8_t* scales,
+                                   hipStream_t st) {
+    if (T <= 0) return hipSuccess;
+    auto rel = [&](int c) { return c < 0 ? -1 : c - col0; };
+    const int segs = (d_in + XM_ROW - 1) / XM_ROW;
+    hipLaunchKernelGGL(xproj_finish_mx4_kernel, dim3(T + T * segs), dim3(1024), 4 * (size_t)ncols_pad * sizeof(float), st,
+                       part, ksplit, T, ncols_pad, rel(se_col), r_s, rs_pad, rel(re_col), n_r, r_r, rr_pad,
+                       rel(router_col), expert, u, v, x, x_dtype, d_in, smooth, inv_smooth, codes, scales);
+    return hipGetLastError();
 }
 
 hipError_t launch_xproj_finish(const float* part, int ksplit, int T, int ncols_pad, int col0, int se_col, int r_s,
@@ -450,7 +499,9 @@ constexpr int RP_TOK = 64;
 constexpr int RP_KG = 128;             // channels per group
 constexpr int RP_MAXN = 5;             // up to 80 projected columns
 
-template <int NBK>  // 16-row blocks of projection rows (ncols = 16*NBK <= 80); also the 16-B pieces per thread
+// NBK: 16-row blocks of projection rows (ncols = 16*NBK <= 80); also the 16-B pieces per thread
+// kAmax: also the partial max |x / s| (microscaled codes need none)
+template <int NBK, bool kAmax>
 __global__ __launch_bounds__(256) void route_pass_kernel(const uint16_t* __restrict__ x, int T, int d_in,
                                                          const uint16_t* __restrict__ mt, int ncols,
                                                          const float* __restrict__ smooth,
@@ -489,7 +540,7 @@ __global__ __launch_bounds__(256) void route_pass_kernel(const uint16_t* __restr
             const int idx = tid + 256 * p, r = idx >> 4, c = idx & 15;
             R.m[p] = *reinterpret_cast<const v4u*>(msrc + (size_t)min(r, max(ncols - 1, 0)) * d_in + k0 + c * 8);
         }
-        R.s = *reinterpret_cast<const v4f*>(((tid & 32) ? inv_smooth : smooth) + k0 + (tid & 31) * 4);
+        if (kAmax) R.s = *reinterpret_cast<const v4f*>(((tid & 32) ? inv_smooth : smooth) + k0 + (tid & 31) * 4);
     };
     auto process = [&](const Regs& R, int g) {
         uint8_t* buf = smem + (g & 1) * BUF;
@@ -498,12 +549,12 @@ __global__ __launch_bounds__(256) void route_pass_kernel(const uint16_t* __restr
             const int idx = tid + 256 * p, r = idx >> 4, c = idx & 15;
             if (r < ncols) *reinterpret_cast<v4u*>(buf + r * 256 + ((c ^ (r & 15)) << 4)) = R.m[p];
         }
-        if (tid < 64) *reinterpret_cast<v4f*>(buf + M_LDS + tid * 16) = R.s;
+        if (kAmax && tid < 64) *reinterpret_cast<v4f*>(buf + M_LDS + tid * 16) = R.s;
         // the stores above are complete in every wave (the other buffer was last read
         // before this barrier); the next group's loads stay in flight
         QE_WAIT_LDS();
         QE_WG_BARRIER();
-        if (rvalid) {
+        if (kAmax && rvalid) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint8_t* sp = buf + M_LDS + (lg * 32 + q * 8) * 4;
@@ -550,6 +601,7 @@ __global__ __launch_bounds__(256) void route_pass_kernel(const uint16_t* __restr
             if (t < T) out[(size_t)t * ncols + n * 16 + lr] = acc[n][r];
         }
     }
+    if (!kAmax) return;
     // a row's 128 channels are spread over lanes lr, lr+16, lr+32, lr+48
     float m = amax;
     m = fmaxf(m, __shfl_xor(m, 16, 64));
@@ -569,15 +621,23 @@ int route_pass_ksplit(int T, int d_in) {
 hipError_t launch_route_pass(const uint16_t* x, int T, int d_in, const uint16_t* mt, int ncols, const float* smooth,
                              const float* inv_smooth, int ksplit, float* part, float* amax_part, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    if (ncols > RP_MAXN * 16 || ncols % 16 || d_in % RP_KG || ksplit < 1 || ksplit > d_in / RP_KG || !smooth ||
-        !inv_smooth)
+    if (ncols > RP_MAXN * 16 || ncols % 16 || d_in % RP_KG || ksplit < 1 || ksplit > d_in / RP_KG ||
+        (amax_part && (!smooth || !inv_smooth)))
         return hipErrorInvalidValue;
     const dim3 grid((T + RP_TOK - 1) / RP_TOK, ksplit);
-#define QE_RP_LAUNCH(NB)                                                                                            \
-    hipLaunchKernelGGL(route_pass_kernel<NB>, grid, dim3(256), 0, st, x, T, d_in, mt, ncols, smooth, inv_smooth, \
-                       ksplit, part, amax_part)
+#define QE_RP_LAUNCH(NB)                                                                                           \
+    if (amax_part)                                                                                                 \
+        hipLaunchKernelGGL((route_pass_kernel<NB, true>), grid, dim3(256), 0, st, x, T, d_in, mt, ncols, smooth,   \
+                           inv_smooth, ksplit, part, amax_part);                                                   \
+    else                                                                                                           \
+        hipLaunchKernelGGL((route_pass_kernel<NB, false>), grid, dim3(256), 0, st, x, T, d_in, mt, ncols, smooth,  \
+                           inv_smooth, ksplit, part, amax_part)
     switch (ncols / 16) {
-        case 0: QE_RP_LAUNCH(0); break;
+        case 0:  // only the maxima
+            if (!amax_part) return hipErrorInvalidValue;
+            hipLaunchKernelGGL((route_pass_kernel<0, true>), grid, dim3(256), 0, st, x, T, d_in, mt, ncols, smooth,
+                               inv_smooth, ksplit, part, amax_part);
+            break;
         case 1: QE_RP_LAUNCH(1); break;
         case 2: QE_RP_LAUNCH(2); break;
         case 3: QE_RP_LAUNCH(3); break;
@@ -784,7 +844,7 @@ __device__ __forceinline__ void route_finish_block(const float* __restrict__ par
         *reinterpret_cast<v4f*>(s_sum + 4 * i) = sum;
     }
     float m = 0.0f;
-    if (tid < nt)
+    if (s_x && tid < nt)
         for (int k = 0; k < ksplit; ++k) m = fmaxf(m, amax_part[(size_t)k * T + t0 + tid]);
     __syncthreads();
     if (tid < nt) {
@@ -810,7 +870,7 @@ __device__ __forceinline__ void route_finish_block(const float* __restrict__ par
                 expert2[t] = e2;
             }
         }
-        s_x[t] = m / (float)qmax;
+        if (s_x) s_x[t] = m / (float)qmax;
     }
     if (u) {
         for (int i = tid; i < nt * rs_pad; i += RF_THREADS) {
@@ -942,11 +1002,12 @@ __device__ __forceinline__ void row_project(const uint16_t* __restrict__ rows, c
 
 // NBS, NBR: 16-column blocks of u (rs_pad / 16) and of v (rr_pad / 16); GPW: channel groups per
 // wave the router's fragments are requested for (2 when d_in <= 4096, else RW_GPW)
-template <int NBS, int NBR, int GPW>
+// kMx: microscaled codes and scales (qmax unused); a quad of threads holds a block
+template <int NBS, int NBR, int GPW, bool kMx>
 __global__ __launch_bounds__(RW_THREADS) void row_prologue_kernel(
     const uint16_t* __restrict__ x, int d_in, const float* __restrict__ smooth, const float* __restrict__ inv_smooth,
     int qmax, const uint16_t* __restrict__ mt, int r_s, int col_router, int n_r, int col_re, int r_r,
-    int8_t* __restrict__ codes, float* __restrict__ s_x, uint16_t* __restrict__ u, int32_t* __restrict__ expert,
+    uint8_t* __restrict__ codes, void* __restrict__ scales, uint16_t* __restrict__ u, int32_t* __restrict__ expert,
     uint16_t* __restrict__ v) {
     __shared__ __attribute__((aligned(16))) uint16_t xl[RW_MAX_DIN];
     __shared__ float s_part[RW_WAVES][64];
@@ -995,13 +1056,15 @@ __global__ __launch_bounds__(RW_THREADS) void row_prologue_kernel(
     if (tid < nch) *reinterpret_cast<v4u*>(xl + tid * 8) = w;
     float xs[8];
     smooth_div8(w, s0, s1, i0, i1, xs);
-    float amax = 0.0f;
-    if (tid < nch) {
+    if constexpr (!kMx) {
+        float amax = 0.0f;
+        if (tid < nch) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, __builtin_fabsf(xs[e]));
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, __builtin_fabsf(xs[e]));
+        }
+        amax = wave_max(amax);
+        if (lane == 0) s_max[wid] = amax;
     }
-    amax = wave_max(amax);
-    if (lane == 0) s_max[wid] = amax;
     QE_WAIT_LDS();
     QE_WG_BARRIER();  // the row and the maxima are in LDS; the router's fragments stay in flight
 
@@ -1010,16 +1073,22 @@ __global__ __launch_bounds__(RW_THREADS) void row_prologue_kernel(
         row_project<1, GPW>(mt + (size_t)col_router * d_in, xl, d_in, wid, lane, rb, true, racc);
         if (lg == 0) s_part[wid][lr] = racc[0][0];
     }
-    // s_x = max |x'| / qmax (a max is exact in any order), then the codes
-    float m = s_max[0];
+    if constexpr (kMx) {
+        if (tid < nch)
+            mx4_store8(xs, codes + (size_t)t * (d_in / 2), reinterpret_cast<uint8_t*>(scales) + (size_t)t * (d_in / kMxBlock),
+                       tid * 8);
+    } else {
+        // s_x = max |x'| / qmax (a max is exact in any order), then the codes
+        float m = s_max[0];
 #pragma unroll
-    for (int q = 1; q < RW_WAVES; ++q) m = fmaxf(m, s_max[q]);
-    const float sx = m / (float)qmax;
-    if (tid == 0) s_x[t] = sx;
-    const float inv_sx = sx != 0.0f ? 1.0f / sx : 0.0f;
-    const bool fast = (sx >= 0x1p-90f && sx <= 0x1p90f) || sx == 0.0f;
-    const v2u cw = codes8(xs, sx, inv_sx, fast, (float)qmax);
-    if (tid < nch) *reinterpret_cast<v2u*>(codes + (size_t)t * d_in + (size_t)tid * 8) = cw;
+        for (int q = 1; q < RW_WAVES; ++q) m = fmaxf(m, s_max[q]);
+        const float sx = m / (float)qmax;
+        if (tid == 0) reinterpret_cast<float*>(scales)[t] = sx;
+        const float inv_sx = sx != 0.0f ? 1.0f / sx : 0.0f;
+        const bool fast = (sx >= 0x1p-90f && sx <= 0x1p90f) || sx == 0.0f;
+        const v2u cw = codes8(xs, sx, inv_sx, fast, (float)qmax);
+        if (tid < nch) *reinterpret_cast<v2u*>(codes + (size_t)t * d_in + (size_t)tid * 8) = cw;
+    }
 
     if constexpr (NBR > 0) {
         // scores summed in wave order by one thread each; then every thread takes the argmin
@@ -1075,23 +1144,28 @@ bool row_prologue_ok(int T, int d_in, int rs_pad, int n_r, int rr_pad) {
 
 hipError_t launch_row_prologue(const uint16_t* x, int T, int d_in, const float* smooth, const float* inv_smooth,
                                int a_bits, const uint16_t* mt, int r_s, int rs_pad, int col_router, int n_r, int col_re,
-                               int r_r, int rr_pad, int8_t* codes, float* s_x, uint16_t* u, int32_t* expert,
+                               int r_r, int rr_pad, void* codes, void* scales, uint16_t* u, int32_t* expert,
                                uint16_t* v, hipStream_t st) {
     if (T <= 0) return hipSuccess;
-    if (!row_prologue_ok(T, d_in, rs_pad, n_r, rr_pad) || !x || !smooth || !inv_smooth || !mt || !codes || !s_x ||
+    if (!row_prologue_ok(T, d_in, rs_pad, n_r, rr_pad) || !x || !smooth || !inv_smooth || !mt || !codes || !scales ||
         (rs_pad > 0 && !u) || (n_r > 0 && (!expert || !v || col_router < 0 || col_re < 0)) || a_bits < 2 ||
         a_bits > 8)
         return hipErrorInvalidValue;
     const dim3 grid(T, rs_pad > 0 ? 2 : 1);
     const int qmax = (1 << (a_bits - 1)) - 1;
     const bool narrow = d_in <= RW_WAVES * 128 * 2;  // at most two channel groups per wave
-#define QE_RW_LAUNCH(S, R)                                                                                          \
-    if (narrow)                                                                                                     \
-        hipLaunchKernelGGL((row_prologue_kernel<S, R, 2>), grid, dim3(RW_THREADS), 0, st, x, d_in, smooth,          \
-                           inv_smooth, qmax, mt, r_s, col_router, n_r, col_re, r_r, codes, s_x, u, expert, v);     \
-    else                                                                                                            \
-        hipLaunchKernelGGL((row_prologue_kernel<S, R, RW_GPW>), grid, dim3(RW_THREADS), 0, st, x, d_in, smooth,     \
-                           inv_smooth, qmax, mt, r_s, col_router, n_r, col_re, r_r, codes, s_x, u, expert, v)
+#define QE_RW_FORM(S, R, G, MX)                                                                                    \
+    hipLaunchKernelGGL((row_prologue_kernel<S, R, G, MX>), grid, dim3(RW_THREADS), 0, st, x, d_in, smooth,         \
+                       inv_smooth, qmax, mt, r_s, col_router, n_r, col_re, r_r, static_cast<uint8_t*>(codes), scales, \
+                       u, expert, v)
+#define QE_RW_LAUNCH(S, R)                      \
+    if (a_bits == 4) {                          \
+        if (narrow) QE_RW_FORM(S, R, 2, true);  \
+        else QE_RW_FORM(S, R, RW_GPW, true);    \
+    } else {                                    \
+        if (narrow) QE_RW_FORM(S, R, 2, false); \
+        else QE_RW_FORM(S, R, RW_GPW, false);   \
+    }
 #define QE_RW_BY_R(S)                          \
     if (rr_pad == 0) {                         \
         QE_RW_LAUNCH(S, 0);                    \
@@ -1109,6 +1183,7 @@ hipError_t launch_row_prologue(const uint16_t* x, int T, int d_in, const float* 
     }
 #undef QE_RW_BY_R
 #undef QE_RW_LAUNCH
+#undef QE_RW_FORM
     return hipGetLastError();
 }
 
@@ -1139,12 +1214,17 @@ constexpr int EQ_FEW_T = 256;       // token counts that take the few-token form
 // exposed fragment load per group); ESL == 0: 1 or 2 experts per pass.  sort_rows == false
 // keeps the tokens in their order (no bucketing, no permutation written): for few tokens
 // whose main product is split over K, whose epilogue does not gain from grouped experts.
-template <int NBR, int ESL>
+// kMx: microscaled codes (a lane's 32 channels of a group are one block), as rows, or (mx_tiled)
+// as the product's tiles in this order, ready to be copied to LDS; s_x and qmax are not used.
+// (4096 x 8192: 42 us, as with integer codes; the block quantization of its own 24 and the tiling 10
+// beside a projection onto every expert's columns, 66 + 40.)
+template <int NBR, int ESL, bool kMx = false>
 __device__ __forceinline__ void expert_quant_tile(
     const uint16_t* __restrict__ x, int T, int d_in, const float* __restrict__ smooth,
     const float* __restrict__ inv_smooth, const float* __restrict__ s_x, int qmax, const int32_t* __restrict__ expert,
     int n_r, const uint16_t* __restrict__ mt_re, int r_r, int ksq, int32_t* __restrict__ perm_out,
-    float* __restrict__ vpart, int8_t* __restrict__ codes, uint16_t* __restrict__ v, bool sort_rows, int tile, int kq) {
+    float* __restrict__ vpart, int8_t* __restrict__ codes, uint16_t* __restrict__ v, bool sort_rows, int tile, int kq,
+    uint8_t* __restrict__ mx_scales = nullptr, bool mx_tiled = false) {
     constexpr int RR = NBR * 16;               // padded routed rank
     constexpr int NB1 = NBR ? NBR : 1;
     constexpr int ESLOTS = ESL > 0 ? ESL : NBR == 4 ? 1 : 2;  // experts per pass
@@ -1240,7 +1320,7 @@ __device__ __forceinline__ void expert_quant_tile(
     const bool valid = t_row >= 0;
     const int t = valid ? t_row : 0;  // rows past T read row 0 and are never stored
     const int e_row = (NBR && valid && routed) ? min(max(expert[t], 0), n_r - 1) : -1;
-    const float sx = valid ? s_x[t] : 0.0f;
+    const float sx = !kMx && valid ? s_x[t] : 0.0f;
     const float inv_sx = sx != 0.0f ? 1.0f / sx : 0.0f;
     const bool fast = (sx >= 0x1p-90f && sx <= 0x1p90f) || sx == 0.0f;
     const float fq = (float)qmax;
@@ -1258,6 +1338,14 @@ __device__ __forceinline__ void expert_quant_tile(
     const int g_beg = (int)((long)kq * ngr / ksq), g_end = (int)((long)(kq + 1) * ngr / ksq);
     const uint16_t* xrow = x + (size_t)t * d_in + lg * 32;
     int8_t* crow = codes + (size_t)t * d_in + lg * 32;
+    // where this lane's block of group 0 goes, and the next group's distance: codes, then the scale
+    const int pos = pos0 + wid * 16 + lr;
+    const size_t rb = (size_t)(pos >> 5) * ngr * 32 + (pos & 31);  // a tiled row's place among the scale dwords
+    uint8_t* mc = reinterpret_cast<uint8_t*>(codes) +
+                  (mx_tiled ? ((size_t)(pos >> 5) * ngr * 128 + lg * 32 + (pos & 31)) * 16 : (size_t)t * (d_in / 2) + lg * 16);
+    uint8_t* ms = mx_scales + (mx_tiled ? rb * 4 + lg : (size_t)t * (d_in / kMxBlock) + lg);
+    const size_t mc_step = mx_tiled ? 2048 : 64, ms_step = mx_tiled ? 128 : 4;
+    const bool m_store = mx_tiled ? pos < (T + 31) / 32 * 32 : valid;  // (a tile's rows past T hold zeros)
 
     v4f acc[NB1];
 #pragma unroll
@@ -1327,17 +1415,24 @@ __device__ __forceinline__ void expert_quant_tile(
             }
             if (first) {
                 v2u cw[4];
+                float xs[4][8];
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const uint8_t* sp = buf + B_LDS + (lg * 32 + s * 8) * 4;
                     const v4f s0 = *reinterpret_cast<const v4f*>(sp), s1 = *reinterpret_cast<const v4f*>(sp + 16);
                     const v4f i0 = *reinterpret_cast<const v4f*>(sp + 512),
                               i1 = *reinterpret_cast<const v4f*>(sp + 528);
-                    float xs[8];
-                    smooth_div8(xv[s], s0, s1, i0, i1, xs);
-                    cw[s] = codes8(xs, sx, inv_sx, fast, fq);
+                    smooth_div8(xv[s], s0, s1, i0, i1, xs[s]);
+                    if constexpr (!kMx) cw[s] = codes8(xs[s], sx, inv_sx, fast, fq);
                 }
-                if (valid) {
+                if constexpr (kMx) {
+                    uint32_t sc;
+                    const v4u c = mx4_codes32(xs, &sc);
+                    if (m_store) {
+                        *reinterpret_cast<v4u*>(mc + g * mc_step) = valid ? c : v4u{0, 0, 0, 0};
+                        ms[g * ms_step] = valid ? (uint8_t)sc : (uint8_t)0;
+                    }
+                } else if (valid) {
                     *reinterpret_cast<v4u*>(crow + k0) = v4u{cw[0][0], cw[0][1], cw[1][0], cw[1][1]};
                     *reinterpret_cast<v4u*>(crow + k0 + 16) = v4u{cw[2][0], cw[2][1], cw[3][0], cw[3][1]};
                 }
@@ -1396,6 +1491,17 @@ __global__ __launch_bounds__(64 * EQ_W) void expert_quant_kernel(
     float* __restrict__ vpart, int8_t* __restrict__ codes, uint16_t* __restrict__ v, bool sort_rows) {
     expert_quant_tile<NBR, ESL>(x, T, d_in, smooth, inv_smooth, s_x, qmax, expert, n_r, mt_re, r_r, ksq, perm_out, vpart,
                                 codes, v, sort_rows, blockIdx.x, blockIdx.y);
+}
+
+template <int NBR, int ESL>
+__global__ __launch_bounds__(64 * EQ_W) void expert_mx4_kernel(
+    const uint16_t* __restrict__ x, int T, int d_in, const float* __restrict__ smooth,
+    const float* __restrict__ inv_smooth, const int32_t* __restrict__ expert, int n_r,
+    const uint16_t* __restrict__ mt_re, int r_r, int ksq, int32_t* __restrict__ perm_out, float* __restrict__ vpart,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, bool tiled, uint16_t* __restrict__ v) {
+    expert_quant_tile<NBR, ESL, true>(x, T, d_in, smooth, inv_smooth, nullptr, 0, expert, n_r, mt_re, r_r, ksq, perm_out,
+                                      vpart, reinterpret_cast<int8_t*>(codes), v, true, blockIdx.x, blockIdx.y, scales,
+                                      tiled);
 }
 
 // the expert-sorted passes of up to RG_MAX linears that read the same x: linear blockIdx.z
@@ -1541,6 +1647,36 @@ hipError_t launch_expert_quant(const uint16_t* x, int T, int d_in, const float* 
     const size_t n = (size_t)T * rr_pad;
     hipLaunchKernelGGL(vpart_finish_kernel, dim3(vpart_finish_blocks(n, ksq)), dim3(256), 0, st, vpart, ksq, T, rr_pad,
                        r_r, keep_order ? nullptr : perm, v);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_mx4(const uint16_t* x, int T, int d_in, const float* smooth, const float* inv_smooth,
+                             const int32_t* expert, int n_r, const uint16_t* mt_re, int rr_pad, int r_r, int ksq,
+                             int32_t* perm, float* vpart, uint8_t* codes, uint8_t* scales, bool tiled, uint16_t* v,
+                             hipStream_t st) {
+    if (T <= 0) return hipSuccess;
+    const int nbr = (expert && v) ? rr_pad / 16 : 0;
+    if ((nbr != 0 && nbr != 2 && nbr != 4) || d_in % EQ_KG || ksq < 1 || ksq > d_in / EQ_KG || n_r > kMaxRouted ||
+        !smooth || !inv_smooth || !codes || !scales || (ksq > 1 && nbr && (!vpart || !perm)))
+        return hipErrorInvalidValue;
+    const dim3 grid((T + EQ_ROWS - 1) / EQ_ROWS, ksq);
+#define QE_EM_LAUNCH(NB, ESLV)                                                                                     \
+    hipLaunchKernelGGL((expert_mx4_kernel<NB, ESLV>), grid, dim3(64 * EQ_W), 0, st, x, T, d_in, smooth, inv_smooth, \
+                       expert, n_r, mt_re, r_r, ksq, perm, vpart, codes, scales, tiled, v)
+    if (nbr == 0) QE_EM_LAUNCH(0, 0);
+    else if (nbr == 2) {
+        if (expert_quant_few(T)) QE_EM_LAUNCH(2, 8);
+        else QE_EM_LAUNCH(2, 0);
+    } else {
+        if (expert_quant_few(T)) QE_EM_LAUNCH(4, 4);
+        else QE_EM_LAUNCH(4, 0);
+    }
+#undef QE_EM_LAUNCH
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || ksq == 1 || !nbr) return err;
+    const size_t n = (size_t)T * rr_pad;
+    hipLaunchKernelGGL(vpart_finish_kernel, dim3(vpart_finish_blocks(n, ksq)), dim3(256), 0, st, vpart, ksq, T, rr_pad,
+                       r_r, perm, v);
     return hipGetLastError();
 }
 

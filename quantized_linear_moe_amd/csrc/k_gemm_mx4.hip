@@ -588,8 +588,10 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
     }
     Mx4Gemm H = G;
     if (P.bm == 256) {
-        const hipError_t e = launch_mx4_tile(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
-        if (e != hipSuccess) return e;
+        if (G.codes) {
+            const hipError_t e = launch_mx4_tile(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
+            if (e != hipSuccess) return e;
+        }
         H.codes = G.a_tiled;
         H.scales = reinterpret_cast<const uint8_t*>(G.a_scale);
     }

@@ -132,6 +132,10 @@ int noalloc_scratch(void** out);
 // Prefill prologue in two reads of x (route pass, then expert-sorted quantization), for
 // bf16 activations; the workspace is sized for it whatever the activation type
 bool two_pass_sized(const qe_linear* lin, int T) { return int_codes(lin) && T > kSkinnyMaxT; }
+// the same two reads for microscaled codes, where there is something to project
+bool mx4_two_pass_sized(const qe_linear* lin, int T) {
+    return mx4(lin) && lin->r_shared + lin->n_routed > 0 && T > kSkinnyMaxT;
+}
 // few-token prefill with bf16 x: the one-launch prologue where its shape limits allow
 bool row_prologue(const qe_linear* lin, int T, int x_dtype) {
     return two_pass_sized(lin, T) && x_dtype == QE_BF16 &&
@@ -195,7 +199,7 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     off = align256(off + (mx4(lin) ? t * (lin->d_in / kMxBlock) : t * 4));
     W.part = off;
     const int xks = std::max({W.xproj_ksplit, T <= kSkinnyMaxT ? skinny_ksplit_proj(lin->d_in) : 1, D.ks_p});
-    const bool two_pass = two_pass_sized(lin, T);
+    const bool two_pass = two_pass_sized(lin, T) || mx4_two_pass_sized(lin, T);
     W.rp_ksplit = two_pass ? route_pass_ksplit(T, lin->d_in) : 0;
     W.eq_ksplit = two_pass ? expert_quant_ksplit(T, lin->d_in) : 0;
     off = align256(off + std::max((size_t)xks * t * P.n_cols_pad, (size_t)W.rp_ksplit * t * P.n_lead) * 4);
@@ -723,6 +727,61 @@ static int run_prologue_rest(const qe_linear* lin, const void* x, int T, int8_t*
     return QE_OK;
 }
 
+// Everything of a microscaled linear before its product: routes, u, v, codes and scales, and the expert
+// order that tiles of many tokens walk (*perm; NULL: token order, also where one tile holds all tokens).
+// *codes, *scales: where to put the rows; NULL on return when the product's tiles were written instead.
+static int run_mx4_prologue(const qe_linear* lin, const void* x, int x_dtype, int T, uint8_t** codes, uint8_t** scales,
+                            uint16_t* u, uint16_t* v, int32_t* expert, int32_t** perm, void* ws, hipStream_t s) {
+    const PrepLayout P = prep_layout(lin);
+    const WsLayout W = ws_layout(lin, T);
+    const Mx4Plan plan = mx4_plan(T, lin->d_in, lin->d_out);
+    const bool route = lin->n_routed > 0;
+    const float* smooth = at<const float>(lin->prep, P.smooth);
+    const float* inv_smooth = at<const float>(lin->prep, P.inv_smooth);
+    const uint16_t* mt = at<const uint16_t>(lin->prep, P.mt);
+    const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
+    // few tokens in one launch; it streams a token's projection rows through one workgroup, which up to 16
+    // tokens pays for narrow rows only (whole forwards of 1 token: 1536 -> 8960 27 us, 32 in three launches;
+    // 3584 -> 18944 43, 44; 8192 -> 29568 88, 77)
+    const bool row = x_dtype == QE_BF16 && (T > kSkinnyMaxT || lin->d_in <= 4096) &&
+                     row_prologue_ok(T, lin->d_in, P.rs_pad, lin->n_routed, P.rr_pad);
+    if (route && T > plan.bm && plan.bm != 0) *perm = at<int32_t>(ws, W.perm);
+    if (!row && x_dtype == QE_BF16 && mx4_two_pass_sized(lin, T)) {  // two reads of x, as for integer codes
+        QE_TRY_HIP(launch_route_pass(xb, T, lin->d_in, mt, P.n_lead, nullptr, nullptr, W.rp_ksplit, at<float>(ws, W.part),
+                                     nullptr, s));
+        QE_TRY_HIP(launch_route_finish(at<const float>(ws, W.part), nullptr, W.rp_ksplit, T, P.n_lead, lin->r_shared,
+                                       P.rs_pad, P.col_router, lin->n_routed, lin->a_bits, expert, u, nullptr, s));
+        const bool tiled = plan.bm == 256;
+        QE_TRY_HIP(launch_expert_mx4(xb, T, lin->d_in, smooth, inv_smooth, expert, lin->n_routed,
+                                     route ? mt + (size_t)P.col_re * lin->d_in : nullptr, P.rr_pad, lin->r_routed,
+                                     W.eq_ksplit, route ? at<int32_t>(ws, W.perm) : nullptr, at<float>(ws, W.vpart),
+                                     tiled ? at<uint8_t>(ws, W.a_tiled) : *codes,
+                                     tiled ? at<uint8_t>(ws, W.a_scale) : *scales, tiled, v, s));
+        if (tiled) *codes = *scales = nullptr;
+        return QE_OK;
+    }
+    if (row) {  // few tokens: one launch, everything in token order
+        QE_TRY_HIP(launch_row_prologue(xb, T, lin->d_in, smooth, inv_smooth, lin->a_bits, mt, lin->r_shared, P.rs_pad,
+                                       P.col_router, lin->n_routed, P.col_re, lin->r_routed, P.rr_pad, *codes, *scales, u,
+                                       expert, v, s));
+    } else if (T <= kSkinnyMaxT && P.n_lead > 0) {
+        float* part = at<float>(ws, W.part);
+        int ks = 0;
+        const int st = xpass_partials(lin, x, x_dtype, T, 0, P.n_cols, P.n_cols_pad, part, ws, s, &ks);
+        if (st) return st;
+        QE_TRY_HIP(launch_xproj_finish_mx4(part, ks, T, P.n_cols_pad, 0, P.col_se, lin->r_shared, P.rs_pad, P.col_re,
+                                           lin->n_routed, lin->r_routed, P.rr_pad, P.col_router, expert, u, v, x, x_dtype,
+                                           lin->d_in, smooth, inv_smooth, *codes, *scales, s));
+    } else {
+        const int st = run_xpass(lin, x, x_dtype, T, u != nullptr, route, route, nullptr, nullptr, expert, u, v, ws, s);
+        if (st) return st;
+        QE_TRY_HIP(launch_mx4_quant(x, x_dtype, smooth, false, T, lin->d_in, *codes, *scales, s));
+    }
+    if (*perm)
+        QE_TRY_HIP(launch_bucket(expert, T, lin->n_routed, at<int32_t>(ws, W.counts), at<int32_t>(ws, W.offsets), *perm, s));
+    return QE_OK;
+}
+
 // keep_order: few tokens may stay in token order in the two-pass prologue (perm is then not
 // written; the caller passes perm == NULL)
 // expert2 (top-2 routing, optional): also the second expert of every token
@@ -794,18 +853,11 @@ int qe_linear_forward(const qe_linear* lin, const void* x, int32_t x_dtype, int3
     uint16_t* u = P.rs_pad > 0 ? at<uint16_t>(ws, W.u) : nullptr;
     uint16_t* v = route ? at<uint16_t>(ws, W.v) : nullptr;
     if (mx4(lin)) {
-        // the adapters' and the router's pass over x, the block quantization, then one product with
-        // both corrections; tiles of many tokens walk them in expert order
-        st = run_xpass(lin, x, x_dtype, T, u != nullptr, route, route, nullptr, nullptr, expert, u, v, ws, s);
+        uint8_t *codes = at<uint8_t>(ws, W.codes), *scales = at<uint8_t>(ws, W.s_x);
+        int32_t* perm = nullptr;
+        st = run_mx4_prologue(lin, x, x_dtype, T, &codes, &scales, u, v, expert, &perm, ws, s);
         if (st) return st;
-        int32_t* perm = route && mx4_plan(T, lin->d_in, lin->d_out).bm != 0 ? at<int32_t>(ws, W.perm) : nullptr;
-        if (perm)
-            QE_TRY_HIP(launch_bucket(expert, T, lin->n_routed, at<int32_t>(ws, W.counts), at<int32_t>(ws, W.offsets),
-                                     perm, s));
-        QE_TRY_HIP(launch_mx4_quant(x, x_dtype, at<const float>(lin->prep, P.smooth), false, T, lin->d_in,
-                                    at<uint8_t>(ws, W.codes), at<uint8_t>(ws, W.s_x), s));
-        return run_mx4_gemm(lin, at<const uint8_t>(ws, W.codes), at<const uint8_t>(ws, W.s_x), T, u, v, expert, perm,
-                            y, ws, s);
+        return run_mx4_gemm(lin, codes, scales, T, u, v, expert, perm, y, ws, s);
     }
     if (T <= kSkinnyMaxT && (lin->a_bits == 16 || lin->w_bits == 4)) {
         // decode: one launch streams the projection matrix and the packed weights, one finishes;

@@ -110,7 +110,7 @@ hipError_t launch_xproj_finish(const float* part, int ksplit, int T, int ncols_p
                                const int32_t* expert_in, float* scores, int32_t* expert_out, uint16_t* u,
                                uint16_t* v, hipStream_t st, int32_t* expert2_out = nullptr);
 
-// two-pass prefill prologue
+// two-pass prefill prologue (microscaled codes need no s_x: amax_part NULL here and s_x NULL in the finish)
 hipError_t launch_route_pass(const uint16_t* x, int T, int d_in, const uint16_t* mt, int ncols, const float* smooth,
                              const float* inv_smooth, int ksplit, float* part, float* amax_part, hipStream_t st);
 int route_pass_ksplit(int T, int d_in);
@@ -143,12 +143,13 @@ struct FinishGroup {
     FinishLinear lin[RG_MAX];
 };
 hipError_t launch_route_finish_group(const FinishGroup& G, int n_lin, int ksplit, int T, hipStream_t st);
-// Few-token prologue in one launch (one workgroup per token, one more for u): codes, s_x, u,
-// routes and v, all in token order; row_prologue_ok says which shapes it takes
+// Few-token prologue in one launch (one workgroup per token, one more for u): codes and scales
+// (int8 and float32 per token; a_bits 4: microscaled blocks), u, routes and v, all in token order;
+// row_prologue_ok says which shapes it takes
 bool row_prologue_ok(int T, int d_in, int rs_pad, int n_r, int rr_pad);
 hipError_t launch_row_prologue(const uint16_t* x, int T, int d_in, const float* smooth, const float* inv_smooth,
                                int a_bits, const uint16_t* mt, int r_s, int rs_pad, int col_router, int n_r, int col_re,
-                               int r_r, int rr_pad, int8_t* codes, float* s_x, uint16_t* u, int32_t* expert,
+                               int r_r, int rr_pad, void* codes, void* scales, uint16_t* u, int32_t* expert,
                                uint16_t* v, hipStream_t st);
 struct EqLinear {
     const float* smooth;

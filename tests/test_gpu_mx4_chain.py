@@ -186,7 +186,7 @@ def test_two_streams_at_once(Q):
             assert torch.equal(o.view(torch.uint8), ref.view(torch.uint8))
 
 
-@pytest.mark.parametrize("cfg_name,lin_name,T", [("qwen2vl_2b", "k", 8), ("qwen2vl_2b", "k", 100), ("qwen2vl_2b", "gate", 1200)])
+@pytest.mark.parametrize("cfg_name,lin_name,T", [("qwen2vl_2b", "k", 8), ("qwen2vl_2b", "k", 100), ("qwen2vl_2b", "gate", 1200), ("qwen2vl_2b", "gate", 1900)])
 def test_linear_forward_graph_replays(Q, cfg_name, lin_name, T):
     L = Q.libqe
     cfg = synth.get_config(cfg_name)
