@@ -550,22 +550,28 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(const float* __restrict
 //     weights themselves bound it up to 12 tokens.  8192 -> 29568: 8 tokens 26 streamed, 29 in 64 x 128 tiles;
 //     16 tokens 34, 31; 32 tokens 53, 36.  29568 -> 8192 (a quarter of the steps per CU): 16 tokens 28, 33;
 //     32 tokens 46, 35.  8192 -> 1024: 32 tokens 13, 15.
-//   * 256 x 256 tiles, one per CU, where they give every CU one: 1024 x 8192 -> 8192 54, 512 tokens (128 x 128) 36.
-//   * 128 x 128 tiles, two per CU: 128 x 8192 -> 29568 47, in 64 x 128 tiles 59; 512 x 8192 -> 8192 36, 40.
+//   * 256 x 256 tiles, one per CU, where they give every CU one, or 128 x 128 tiles would need a second round of
+//     two per CU: 512 x 8192 -> 29568 80 (128 x 128: 132), 512 x 3584 -> 18944 35 (44), 1024 x 1536 -> 8960 24
+//     (30); 1024 x 8192 -> 8192, where they would not, 52 (49); 2048 x 4096 -> 4096 35 (32).
+//   * 128 x 128 tiles, two per CU: 128 x 8192 -> 29568 42, in 64 x 128 tiles 59; 512 x 8192 -> 8192 36, 40.  Fewer of
+//     them with long sums, split where half the CUs would be idle: 640 x 18944 -> 3584 47 (64 x 128: 61),
+//     320 x 18944 -> 3584 in 3 splits 35 (40), 256 x 29568 -> 8192 in 2 60 (73), 128 x 29568 -> 8192 in 4 48 (52);
+//     with 8192 tile steps 256 x 8192 -> 8192 28 (24), with 7168 256 x 14336 -> 4096 27 (24).
 //   * 64 x 128 tiles: 32 x 8192 -> 29568 36, in 128 x 128 tiles 43.  Long sums in few tiles are split:
-//     128 x 29568 -> 8192 76 unsplit, 53 in 2 or 4; 64 x 29568 -> 8192 80, 53, 41.
+//     64 x 29568 -> 8192 80 unsplit, 53 in 2, 41 in 4.
 //   * 64 x 64 tiles, split until there are about 512: 128 x 18944 -> 3584 40 unsplit, 23 split.
 Mx4Plan mx4_plan(int T, int d_in, int d_out) {
     Mx4Plan P{0, 0, 1};
     const int KB = d_in / 128, wgs = (int)(((long)d_out + 31) / 32);
     if (T <= 12 || (T <= kMxMaxTStream && (long)((wgs + 255) / 256) * KB * T <= 3800)) return P;
     auto tiles = [&](int bm, int bn) { return ((long)T + bm - 1) / bm * (((long)d_out + bn - 1) / bn); };
-    const long t128 = tiles(64, 128), t64 = tiles(64, 64);
-    if (tiles(256, 256) >= 256 && KB >= 8) P = {256, 256, 1};
-    else if (T > 64 && tiles(128, 128) >= 192) P = {128, 128, 1};
-    else if (t128 >= 200) P = {64, 128, 1};
-    else if (t128 >= 50 && KB >= 64) P = {64, 128, (int)std::min(512 / t128, 4l)};
-    else P = {64, 64, (int)std::max(1l, std::min(512 / std::min(t64, 512l), (long)KB / 8))};
+    const long t128x128 = tiles(128, 128), t64x128 = tiles(64, 128), t64x64 = tiles(64, 64);
+    if (KB >= 8 && (tiles(256, 256) >= 256 || (T > 128 && t128x128 > 512))) P = {256, 256, 1};
+    else if (T > 64 && t128x128 >= 192) P = {128, 128, 1};
+    else if (T > 64 && t128x128 * KB >= 11000) P = {128, 128, (int)std::max(1l, std::min(256 / t128x128, 4l))};
+    else if (t64x128 >= 200) P = {64, 128, 1};
+    else if (t64x128 >= 50 && KB >= 64) P = {64, 128, (int)std::min(512 / t64x128, 4l)};
+    else P = {64, 64, (int)std::max(1l, std::min(512 / std::min(t64x64, 512l), (long)KB / 8))};
     return P;
 }
 
@@ -587,7 +593,8 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
         return hipGetLastError();
     }
     Mx4Gemm H = G;
-    if (P.bm == 256) {
+    const bool tiled = !G.codes || mx4_tiled(P, G.d_in);
+    if (tiled) {
         if (G.codes) {
             const hipError_t e = launch_mx4_tile(G.codes, G.scales, G.perm, G.T, G.d_in, G.a_tiled, G.a_scale, st);
             if (e != hipSuccess) return e;
@@ -608,7 +615,8 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& G, const Mx4Plan& P, hipStream_t st) {
         if (main * 256 < G.d_out)
             launch(gemm_mx4_kernel<128, 128, 2, 2, true, 4>, 128, 128, 256, main * 256, (G.d_out - main * 256 + 127) / 128);
     } else if (P.bm == 128) {
-        launch(gemm_mx4_kernel<128, 128, 2, 2, false, 4>, 128, 128, 256, 0, columns);
+        if (tiled) launch(gemm_mx4_kernel<128, 128, 2, 2, true, 4>, 128, 128, 256, 0, columns);
+        else launch(gemm_mx4_kernel<128, 128, 2, 2, false, 4>, 128, 128, 256, 0, columns);
     } else if (P.bn == 128) {
         launch(gemm_mx4_kernel<64, 128, 2, 2, false, 4>, 64, 128, 256, 0, columns);
     } else {

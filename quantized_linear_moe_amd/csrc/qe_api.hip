@@ -227,7 +227,7 @@ WsLayout ws_layout(const qe_linear* lin, int T) {
     const int skinny_parts = mx4(lin) && W.skinny_ksplit == 1 ? 0 : W.skinny_ksplit;
     off = align256(off + (size_t)std::max({skinny_parts, D.ks_m, W.gemm_ksplit > 1 ? W.gemm_ksplit : 0}) * t *
                              lin->d_out * 4);
-    const bool tiles = mx4(lin) && mx4_plan(T, lin->d_in, lin->d_out).bm == 256;
+    const bool tiles = mx4(lin) && mx4_plan(T, lin->d_in, lin->d_out).bm >= 128;
     W.a_tiled = off;
     off = align256(off + (tiles ? mx4_tile_codes(t, lin->d_in) : 0));
     W.a_scale = off;
@@ -751,7 +751,7 @@ static int run_mx4_prologue(const qe_linear* lin, const void* x, int x_dtype, in
                                      nullptr, s));
         QE_TRY_HIP(launch_route_finish(at<const float>(ws, W.part), nullptr, W.rp_ksplit, T, P.n_lead, lin->r_shared,
                                        P.rs_pad, P.col_router, lin->n_routed, lin->a_bits, expert, u, nullptr, s));
-        const bool tiled = plan.bm == 256;
+        const bool tiled = plan.bm >= 128;  // (the pass writes tiles as fast as rows)
         QE_TRY_HIP(launch_expert_mx4(xb, T, lin->d_in, smooth, inv_smooth, expert, lin->n_routed,
                                      route ? mt + (size_t)P.col_re * lin->d_in : nullptr, P.rr_pad, lin->r_routed,
                                      W.eq_ksplit, route ? at<int32_t>(ws, W.perm) : nullptr, at<float>(ws, W.vpart),

@@ -123,6 +123,10 @@ struct Mx4Plan {
     int ksplit;
 };
 Mx4Plan mx4_plan(int T, int d_in, int d_out);
+// Whether its activations come as tiles.  Making them is a launch (3 us, 10 at 4096 x 8192), for 128-token
+// tiles worth it on long sums: 512 x 29568 -> 8192 113 us from rows, 88 from tiles; 1024 x 8192 -> 8192 53, 49;
+// 2048 x 4096 -> 4096 31.7, 32.3; 384 x 3584 -> 18944 32, 37.
+inline bool mx4_tiled(const Mx4Plan& P, int d_in) { return P.bm == 256 || (P.bm == 128 && d_in >= 8192); }
 
 struct Mx4Gemm {
     const uint8_t* codes;      // [T][d_in/2] or NULL
