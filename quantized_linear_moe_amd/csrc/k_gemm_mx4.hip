@@ -552,8 +552,9 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(const float* __restrict
 //     32 tokens 46, 35.  8192 -> 1024: 32 tokens 13, 15.
 //   * 256 x 256 tiles, one per CU, where they give every CU one, or 128 x 128 tiles would need a second round of
 //     two per CU: 512 x 8192 -> 29568 80 (128 x 128: 132), 512 x 3584 -> 18944 35 (44), 1024 x 1536 -> 8960 24
-//     (30); 1024 x 8192 -> 8192, where they would not, 52 (49); 2048 x 4096 -> 4096 35 (32).
-//   * 128 x 128 tiles, two per CU: 128 x 8192 -> 29568 42, in 64 x 128 tiles 59; 512 x 8192 -> 8192 36, 40.  Fewer of
+//     (30); 1024 x 8192 -> 8192, where they would not, 52 (49); 2048 x 4096 -> 4096 35 (32).  Not for up to
+//     128 tokens: 100 x 3584 -> 151936 118 (103), 64 of them 93 (64 x 128: 69).
+//   * 128 x 128 tiles, two per CU: 128 x 8192 -> 29568 42, in 64 x 128 tiles 59; 512 x 8192 -> 8192 31, 34.  Fewer of
 //     them with long sums, split where half the CUs would be idle: 640 x 18944 -> 3584 47 (64 x 128: 61),
 //     320 x 18944 -> 3584 in 3 splits 35 (40), 256 x 29568 -> 8192 in 2 60 (73), 128 x 29568 -> 8192 in 4 48 (52);
 //     with 8192 tile steps 256 x 8192 -> 8192 28 (24), with 7168 256 x 14336 -> 4096 27 (24).
@@ -566,7 +567,7 @@ Mx4Plan mx4_plan(int T, int d_in, int d_out) {
     if (T <= 12 || (T <= kMxMaxTStream && (long)((wgs + 255) / 256) * KB * T <= 3800)) return P;
     auto tiles = [&](int bm, int bn) { return ((long)T + bm - 1) / bm * (((long)d_out + bn - 1) / bn); };
     const long t128x128 = tiles(128, 128), t64x128 = tiles(64, 128), t64x64 = tiles(64, 64);
-    if (KB >= 8 && (tiles(256, 256) >= 256 || (T > 128 && t128x128 > 512))) P = {256, 256, 1};
+    if (KB >= 8 && T > 128 && (tiles(256, 256) >= 256 || t128x128 > 512)) P = {256, 256, 1};
     else if (T > 64 && t128x128 >= 192) P = {128, 128, 1};
     else if (T > 64 && t128x128 * KB >= 11000) P = {128, 128, (int)std::max(1l, std::min(256 / t128x128, 4l))};
     else if (t64x128 >= 200) P = {64, 128, 1};

@@ -184,6 +184,7 @@ SHAPES = [  # T, d_in, d_out, r_s, n_r, r_r
     (4099, 128, 4112, 8, 4, 8), (40, 512, 25616, 32, 8, 32), (100, 8192, 3216, 32, 8, 32), (17, 8192, 528, 16, 4, 64),
     (257, 1152, 16400, 8, 16, 32), (4352, 1024, 4112, 32, 8, 32), (48, 1024, 4112, 64, 16, 64),
     (130, 1152, 32800, 32, 8, 32), (200, 8192, 12304, 8, 4, 32), (70, 29568, 6160, 0, 8, 16), (150, 14336, 5136, 32, 0, 0),
+    (100, 1024, 65552, 8, 4, 8), (17, 1024, 65552, 0, 0, 0),
 ]
 
 
