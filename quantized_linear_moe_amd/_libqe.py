@@ -295,28 +295,30 @@ def qe_linear_forward_noalloc(lin, x, y, expert_out, stream=None):
                                           _ptr(expert_out), _stream(stream)), "qe_linear_forward_noalloc")
 
 
-def _on(where, *args):
-    """Checks the arguments of a device call: (name, tensor, shape, dtype) each, tensor None where it
-    may be left out; all dense, on the device of the first.  Returns that device's index."""
-    index = args[0][1].get_device()
-    for name, t, shape, dtype in args:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{where}: {name} must have shape {shape}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
-        if t.get_device() != index:
-            raise ValueError(f"{where}: {name} is on {t.device}, not {args[0][1].device}")
-    if index < 0:
-        raise ValueError(f"{where}: needs device tensors, got {args[0][1].device}")
-    return index
+def _refuse(where, name, t, shape, dtype, index):
+    if t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    raise ValueError(f"{where}: {name} is on {t.device}, not on device {index}")
+
+
+def _arg(where, name, t, shape, dtype, index):
+    """The address of a device argument, None where it is left out: of this shape and type, dense, on device
+    `index`."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(where, name, t, shape, dtype, index)
+    return t.data_ptr()
 
 
 def _call_on(index, where, fn, *args, stream=None):
     """fn(*args, stream) with the tensors' device current, on `stream` or that device's current one."""
+    if index < 0:
+        raise ValueError(f"{where}: needs device tensors")
     # the raw handle: making a torch.cuda.Stream for it takes as long as a small launch
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch.cuda.current_device():
@@ -331,64 +333,67 @@ def _call_on(index, where, fn, *args, stream=None):
 def qe_mx4_quant(x, smooth, codes, scales, multiply=False, stream=None):
     """Enqueue the microscaled 4-bit form of x / smooth (multiply: x * smooth; smooth may be None):
     codes uint8 [T, d // 2], scales uint8 [T, d // 32]."""
-    T, d = x.shape
-    dev = _on("qe_mx4_quant", ("x", x, (T, d), x.dtype), ("smooth", smooth, (d,), torch.float32),
-              ("codes", codes, (T, d // 2), torch.uint8), ("scales", scales, (T, d // 32), torch.uint8))
-    _call_on(dev, "qe_mx4_quant", _lib.qe_mx4_quant, _ptr(x), _dtype_code(x), _ptr(smooth), int(multiply), T, d,
-             _ptr(codes), _ptr(scales), stream=stream)
+    f, dev, (T, d) = "qe_mx4_quant", x.get_device(), x.shape
+    px = _arg(f, "x", x, x.shape, x.dtype, dev)
+    ps = _arg(f, "smooth", smooth, (d,), torch.float32, dev)
+    pc = _arg(f, "codes", codes, (T, d // 2), torch.uint8, dev)
+    pe = _arg(f, "scales", scales, (T, d // 32), torch.uint8, dev)
+    _call_on(dev, f, _lib.qe_mx4_quant, px, _dtype_code(x), ps, int(multiply), T, d, pc, pe, stream=stream)
 
 
 def qe_mx4_dequant(codes, scales, x, stream=None):
     """Enqueue x (bf16 or float32 [T, d]) = the values of microscaled codes and scales."""
-    T, d = x.shape
-    dev = _on("qe_mx4_dequant", ("x", x, (T, d), x.dtype), ("codes", codes, (T, d // 2), torch.uint8),
-              ("scales", scales, (T, d // 32), torch.uint8))
-    _call_on(dev, "qe_mx4_dequant", _lib.qe_mx4_dequant, _ptr(codes), _ptr(scales), T, d, _ptr(x), _dtype_code(x),
-             stream=stream)
+    f, dev, (T, d) = "qe_mx4_dequant", x.get_device(), x.shape
+    px = _arg(f, "x", x, x.shape, x.dtype, dev)
+    pc = _arg(f, "codes", codes, (T, d // 2), torch.uint8, dev)
+    pe = _arg(f, "scales", scales, (T, d // 32), torch.uint8, dev)
+    _call_on(dev, f, _lib.qe_mx4_dequant, pc, pe, T, d, px, _dtype_code(x), stream=stream)
 
 
 def qe_mx4_prepare(lin: qe_linear, w_codes, w_scales, smooth, A_s, B_s, A_r, B_r, R, prep, stream=None):
     """qe_prepare for a linear with a_bits 4 (w_codes, w_scales: qe_mx4_quant of its weights)."""
-    bf, i, o, rs, n, rr = torch.bfloat16, lin.d_in, lin.d_out, lin.r_shared, lin.n_routed, lin.r_routed
-    dev = _on("qe_mx4_prepare", ("w_codes", w_codes, (o, i // 2), torch.uint8),
-              ("w_scales", w_scales, (o, i // 32), torch.uint8), ("smooth", smooth, (i,), torch.float32),
-              ("A_s", A_s, (i, rs), bf), ("B_s", B_s, (rs, o), bf), ("A_r", A_r, (n, i, rr), bf),
-              ("B_r", B_r, (n, rr, o), bf), ("R", R, (i, n), bf), ("prep", prep, tuple(prep.shape), torch.uint8))
+    f, dev, bf, u8 = "qe_mx4_prepare", w_codes.get_device(), torch.bfloat16, torch.uint8
+    i, o, rs, n, rr = lin.d_in, lin.d_out, lin.r_shared, lin.n_routed, lin.r_routed
+    p = [_arg(f, name, t, shape, dtype, dev) for name, t, shape, dtype in (
+        ("w_codes", w_codes, (o, i // 2), u8), ("w_scales", w_scales, (o, i // 32), u8),
+        ("smooth", smooth, (i,), torch.float32), ("A_s", A_s, (i, rs), bf), ("B_s", B_s, (rs, o), bf),
+        ("A_r", A_r, (n, i, rr), bf), ("B_r", B_r, (n, rr, o), bf), ("R", R, (i, n), bf), ("prep", prep, prep.shape, u8))]
     need = qe_prepared_bytes(lin)
     if prep.numel() < need:
         raise ValueError(f"qe_mx4_prepare: prep holds {prep.numel()} bytes of {need}")
-    _call_on(dev, "qe_mx4_prepare", _lib.qe_mx4_prepare, ctypes.byref(lin), _ptr(w_codes), _ptr(w_scales),
-             _ptr(smooth), _ptr(A_s), _ptr(B_s), _ptr(A_r), _ptr(B_r), _ptr(R), _ptr(prep), stream=stream)
+    _call_on(dev, f, _lib.qe_mx4_prepare, ctypes.byref(lin), *p, stream=stream)
 
 
 def qe_mx4_gemm(lin: qe_linear, codes, scales, u, v, expert, y, ws, perm=None, stream=None):
     """Enqueue y = the product of microscaled activations [T, d_in] and the prepared weights, plus the
     shared (u) and routed (v, expert) low-rank terms where given (rows padded to rank_pad)."""
-    T = codes.shape[0]
-    dev = _on("qe_mx4_gemm", ("codes", codes, (T, lin.d_in // 2), torch.uint8),
-              ("scales", scales, (T, lin.d_in // 32), torch.uint8),
-              ("u", u, (T, rank_pad(lin.r_shared)), torch.bfloat16),
-              ("v", v, (T, rank_pad(lin.r_routed)), torch.bfloat16), ("expert", expert, (T,), torch.int32),
-              ("perm", perm, (T,), torch.int32),
-              ("y", y, (T, lin.d_out), torch.bfloat16 if lin.y_dtype == QE_BF16 else torch.float32),
-              ("ws", ws, tuple(ws.shape), ws.dtype))
-    _call_on(dev, "qe_mx4_gemm", _lib.qe_mx4_gemm, ctypes.byref(lin), _ptr(codes), _ptr(scales), T, _ptr(u), _ptr(v),
-             _ptr(expert), _ptr(perm), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), stream=stream)
+    f, dev, T, d_in = "qe_mx4_gemm", codes.get_device(), codes.shape[0], lin.d_in
+    pc = _arg(f, "codes", codes, (T, d_in // 2), torch.uint8, dev)
+    ps = _arg(f, "scales", scales, (T, d_in // 32), torch.uint8, dev)
+    pu = None if u is None else _arg(f, "u", u, (T, rank_pad(lin.r_shared)), torch.bfloat16, dev)
+    pv = None if v is None else _arg(f, "v", v, (T, rank_pad(lin.r_routed)), torch.bfloat16, dev)
+    pe = _arg(f, "expert", expert, (T,), torch.int32, dev)
+    pp = _arg(f, "perm", perm, (T,), torch.int32, dev)
+    py = _arg(f, "y", y, (T, lin.d_out), torch.bfloat16 if lin.y_dtype == QE_BF16 else torch.float32, dev)
+    pw = _arg(f, "ws", ws, ws.shape, ws.dtype, dev)
+    _call_on(dev, f, _lib.qe_mx4_gemm, ctypes.byref(lin), pc, ps, T, pu, pv, pe, pp, py, pw, ws.nbytes, stream=stream)
 
 
 def qe_add_rmsnorm(x, res, weight, eps, h=None, xn=None, smooth=None, a_bits=0, codes=None, scales=None, stream=None):
     """Enqueue h = x + res (res may be None), xn = RMS norm of h times weight, and with a_bits 4, 6 or 8
     the codes and scales of xn / smooth (see include/qe.h; outputs left out are None)."""
-    T, d = x.shape
-    mx = a_bits == 4
-    dev = _on("qe_add_rmsnorm", ("x", x, (T, d), x.dtype), ("res", res, (T, d), x.dtype),
-              ("weight", weight, (d,), weight.dtype), ("h", h, (T, d), x.dtype), ("xn", xn, (T, d), x.dtype),
-              ("smooth", smooth, (d,), torch.float32),
-              ("codes", codes, (T, d // 2 if mx else d), torch.uint8 if mx else torch.int8),
-              ("scales", scales, (T, d // 32) if mx else (T,), torch.uint8 if mx else torch.float32))
-    _call_on(dev, "qe_add_rmsnorm", _lib.qe_add_rmsnorm, _ptr(x), _ptr(res), _dtype_code(x), _ptr(weight),
-             _dtype_code(weight), eps, T, d, _ptr(h), _ptr(xn), _ptr(smooth), a_bits, _ptr(codes), _ptr(scales),
-             stream=stream)
+    f, dev, shape, dt, mx = "qe_add_rmsnorm", x.get_device(), x.shape, x.dtype, a_bits == 4
+    T, d = shape
+    px = _arg(f, "x", x, shape, dt, dev)
+    pr = _arg(f, "res", res, shape, dt, dev)
+    pw = _arg(f, "weight", weight, (d,), weight.dtype, dev)
+    ph = _arg(f, "h", h, shape, dt, dev)
+    pn = _arg(f, "xn", xn, shape, dt, dev)
+    ps = _arg(f, "smooth", smooth, (d,), torch.float32, dev)
+    pc = _arg(f, "codes", codes, (T, d // 2) if mx else shape, torch.uint8 if mx else torch.int8, dev)
+    pe = _arg(f, "scales", scales, (T, d // 32) if mx else (T,), torch.uint8 if mx else torch.float32, dev)
+    _call_on(dev, f, _lib.qe_add_rmsnorm, px, pr, _dtype_code(x), pw, _dtype_code(weight), eps, T, d, ph, pn, ps, a_bits,
+             pc, pe, stream=stream)
 
 
 def qe_colmean_abs(W, w, stream=None):
