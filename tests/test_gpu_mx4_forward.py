@@ -116,3 +116,35 @@ def test_routes_and_corrections(Q, shape):
     tol = 2.0 ** -8 * value + 3 * (d_in + 64) * 2.0 ** -23 * terms
     err = np.abs(y.double().cpu().numpy() - ref)
     assert np.all(err <= tol), float((err / np.maximum(tol, 1e-30)).max())
+
+
+@pytest.mark.parametrize("shape", [SHAPES[i] for i in (0, 1, 2, 4, 6, 8, 9, 12, 16, 18, 19)], ids=ids)
+def test_graph_replays(Q, shape):
+    """Captured once and replayed on new inputs, between eager forwards of the same linear in the same workspace."""
+    L = Q.libqe
+    T, d_in, d_out = shape[:3]
+    rng, x0, p = _case(shape)
+    w = torch.from_numpy(rng.integers(0, 256, (d_out, d_in // 2)).astype(np.uint8)).to(DEV)
+    layer = _layer(Q, p, w, torch.from_numpy(rng.integers(118, 124, (d_out, d_in // 32)).astype(np.uint8)).to(DEV))
+    ws = layer.workspace(T)
+
+    def run(x):
+        y = torch.empty(T, d_out, device=DEV)
+        e = torch.zeros(T, dtype=torch.int32, device=DEV)
+        L.qe_linear_forward(layer.lin, x, y, e, ws)
+        return y, e
+
+    inputs = [x0, -x0, x0.flip(0).contiguous(), 0.5 * x0]
+    eager = [run(x) for x in inputs]
+    x = x0.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, e = run(x)
+    for i in (1, 2, 0, 3, 3):
+        x.copy_(inputs[i])
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager[i][0]) and torch.equal(e, eager[i][1])
+        again = run(inputs[(i + 1) % 4])
+        assert torch.equal(again[0], eager[(i + 1) % 4][0])
