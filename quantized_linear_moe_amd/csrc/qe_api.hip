@@ -727,8 +727,9 @@ static int run_prologue_rest(const qe_linear* lin, const void* x, int T, int8_t*
     return QE_OK;
 }
 
-// Everything of a microscaled linear before its product: routes, u, v, codes and scales, and the expert
-// order that tiles of many tokens walk (*perm; NULL: token order, also where one tile holds all tokens).
+// Everything of a microscaled linear before its product: routes, u, v, codes and scales, and the order that
+// the product's tiles are in (*perm; NULL: token order).  Rows are walked in expert order where the tokens
+// fill more than one tile; tiles written here are in expert order whatever the token count.
 // *codes, *scales: where to put the rows; NULL on return when the product's tiles were written instead.
 static int run_mx4_prologue(const qe_linear* lin, const void* x, int x_dtype, int T, uint8_t** codes, uint8_t** scales,
                             uint16_t* u, uint16_t* v, int32_t* expert, int32_t** perm, void* ws, hipStream_t s) {
@@ -745,13 +746,14 @@ static int run_mx4_prologue(const qe_linear* lin, const void* x, int x_dtype, in
     // 3584 -> 18944 43, 44; 8192 -> 29568 88, 77)
     const bool row = x_dtype == QE_BF16 && (T > kSkinnyMaxT || lin->d_in <= 4096) &&
                      row_prologue_ok(T, lin->d_in, P.rs_pad, lin->n_routed, P.rr_pad);
-    if (route && T > plan.bm && plan.bm != 0) *perm = at<int32_t>(ws, W.perm);
-    if (!row && x_dtype == QE_BF16 && mx4_two_pass_sized(lin, T)) {  // two reads of x, as for integer codes
+    const bool two_pass = !row && x_dtype == QE_BF16 && mx4_two_pass_sized(lin, T);
+    const bool tiled = two_pass && plan.bm >= 128;  // (the second pass writes tiles as fast as rows)
+    if (route && (tiled || (plan.bm != 0 && T > plan.bm))) *perm = at<int32_t>(ws, W.perm);
+    if (two_pass) {  // two reads of x, as for integer codes
         QE_TRY_HIP(launch_route_pass(xb, T, lin->d_in, mt, P.n_lead, nullptr, nullptr, W.rp_ksplit, at<float>(ws, W.part),
                                      nullptr, s));
         QE_TRY_HIP(launch_route_finish(at<const float>(ws, W.part), nullptr, W.rp_ksplit, T, P.n_lead, lin->r_shared,
                                        P.rs_pad, P.col_router, lin->n_routed, lin->a_bits, expert, u, nullptr, s));
-        const bool tiled = plan.bm >= 128;  // (the pass writes tiles as fast as rows)
         QE_TRY_HIP(launch_expert_mx4(xb, T, lin->d_in, smooth, inv_smooth, expert, lin->n_routed,
                                      route ? mt + (size_t)P.col_re * lin->d_in : nullptr, P.rr_pad, lin->r_routed,
                                      W.eq_ksplit, route ? at<int32_t>(ws, W.perm) : nullptr, at<float>(ws, W.vpart),
