@@ -150,7 +150,8 @@ size_t qe_workspace_bytes(const qe_linear* lin, int32_t T);
  * activation quantization; A6/A8 from the listing's Tables 1-3.  In float32 with
  * IEEE division and round-half-to-even:
  *   x'[t][j] = x[t][j] / s[j];  s_x[t] = max_j |x'[t][j]| / qmax  (qmax 31 or 127)
- *   codes[t][j] = clamp(rint(x'[t][j] / s_x[t]), -qmax, qmax); all-zero token -> 0
+ *   codes[t][j] = clamp(rint(x'[t][j] / s_x[t]), -qmax, qmax); s_x[t] = 0 (all-zero token) -> 0;
+ *   a NaN is left out of the maximum and gets -qmax
  * x: device [T][d_in] (x_dtype); smooth: device [d_in] or NULL (identity);
  * codes: device int8 [T][d_in]; s_x: device float32 [T].  a_bits 6 or 8; d_in % 8 == 0 and
  * d_in <= 32768 (else QE_ERR_UNSUPPORTED).

@@ -170,7 +170,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, const 
             for (int it = 0; it < IT; ++it) {
                 const int j = (it * nthr + threadIdx.x) * 8;
                 if (j >= d) continue;
-                *reinterpret_cast<v2u*>(codes + row + j) = quant8(v[it], sx);
+                *reinterpret_cast<v2u*>(codes + row + j) = quant8(v[it], sx, (float)qmax);
             }
         }
     }
