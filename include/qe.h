@@ -312,8 +312,9 @@ int qe_linear_forward_noalloc(const qe_linear* lin, const void* x, int32_t x_dty
  *   scales  uint8 [T][d/32]: the block's scale is 2^(byte - 127); 255 is NaN
  * Quantization of a block with largest magnitude amax: byte = floor(log2 amax) - 2 + 127, at least 0
  * (0 for a zero block); code = the nearest entry to |value| / scale, a value halfway between two
- * taking the even index, values above 6 taking 6.  A block that holds a NaN or an infinity gets byte
- * 255 and zero codes, so it reads back as NaN and makes the products that use it NaN.
+ * taking the even index, values above 6 taking 6, with the value's sign (also on zeros).  A block that
+ * holds a NaN or an infinity gets byte 255 and zero codes, so it reads back as NaN and makes the products
+ * that use it NaN.
  *
  * qe_mx4_quant: codes and scales of x / smooth (multiply 0: activations) or x * smooth (multiply 1:
  *   weights), in float32 with IEEE division; smooth NULL: of x.  x device [T][d] (x_dtype), smooth device

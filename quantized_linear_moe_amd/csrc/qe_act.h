@@ -11,11 +11,12 @@ __device__ inline float bf16_bits_to_f32(uint32_t h) { return __uint_as_float(h 
 // a / b correctly rounded, given inv_b = RN(1/b).  One multiply and two fused
 // multiply-adds (Markstein's correction).  Exact for |a| in [2^-100, 2^100] and b
 // in [2^-90, 2^90] with quotients of magnitude >= 2^-3; callers fall back to the
-// IEEE division outside that domain.
+// IEEE division outside that domain.  The remainder is taken as b q0 - a: of a zero it is +0, and the last
+// step, q0 - 0, keeps q0's sign (a - b q0 would turn -0 / b into +0).
 __device__ inline float div_markstein(float a, float b, float inv_b) {
     float q0 = a * inv_b;
-    float r = __builtin_fmaf(-b, q0, a);
-    return __builtin_fmaf(r, inv_b, q0);
+    float r = __builtin_fmaf(b, q0, -a);
+    return __builtin_fmaf(-r, inv_b, q0);
 }
 
 __device__ inline bool in_markstein_range(float a) {
