@@ -71,7 +71,8 @@ typedef enum { QE_F32 = 0, QE_BF16 = 1 } qe_dtype;
  *                (the bf16-output option of the decode settings, listing Tables 1-3 and 8);
  *                every `float* y` argument of the calls below then points at bf16 elements.
  *                qe_routed_lora and qe_linear_forward_top2 add into y and take QE_F32 only.
- *   prep         device buffer written by qe_prepare() (qe_prepared_bytes() bytes)
+ *   prep         device buffer written by qe_prepare(), or with a_bits 4 by qe_mx4_prepare()
+ *                (qe_prepared_bytes() bytes)
  * Kernel-path constraints: d_out % 16 == 0 and d_in % 128 == 0, and d_in <= 32768 when
  * a_bits is 6 or 8; with a_bits 4, d_out and the tokens of a call are at most 2^30 (else
  * QE_ERR_UNSUPPORTED, and 0 from the sizing calls).
@@ -127,10 +128,13 @@ size_t qe_prepared_bytes(const qe_linear* lin);
  * the canonical layouts:
  *   w_packed  W4/W3 packed codes as produced by qe_pack_weights
  *   w_scale   float32 [d_out]
- *   smooth    float32 [d_in], entries > 0, or NULL (identity); must be NULL when a_bits == 16
+ *   smooth    float32 [d_in], entries > 0 (normal numbers, at least 2^-126: their reciprocals are
+ *             kept beside them), or NULL (identity); must be NULL when a_bits == 16
  *   A_s [d_in][r_shared], B_s [r_shared][d_out]          bf16 (NULL iff r_shared == 0)
  *   A_r [n_routed][d_in][r_routed], B_r [n_routed][r_routed][d_out]  bf16
  *   R   [d_in][n_routed]                                  bf16 (NULL iff n_routed == 0)
+ * Adapter and router entries are finite: the kernels multiply an expert's entries also by the zeros that
+ * stand for its neighbours' tokens.
  * prep: device output buffer of qe_prepared_bytes(lin) bytes; it becomes lin->prep.
  * The inputs may be freed once the enqueued work has finished.
  */
@@ -361,6 +365,9 @@ int qe_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_t* scale
  * least one of h, xn and codes is).  In place: h or xn may be x or res itself (both may not be one
  * buffer); no other overlap.  eps > 0.  d % 8 == 0 (d % 32 == 0 for a_bits 4) and d <= 32768, else
  * QE_ERR_UNSUPPORTED.
+ * With a_bits 4 the codes save qe_mx4_gemm's callers a pass.  A linear with corrections also needs the routes
+ * and adapter inputs of xn: there qe_linear_forward on xn, which makes them in its own passes, is faster than
+ * qe_route, qe_adapter_inputs and qe_mx4_gemm on these codes.
  */
 int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* weight, int32_t weight_dtype,
                    float eps, int32_t T, int32_t d, void* h, void* xn, const float* smooth, int32_t a_bits, void* codes,

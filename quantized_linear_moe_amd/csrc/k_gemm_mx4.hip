@@ -65,7 +65,8 @@ __device__ inline void store_out(float* y, size_t idx, float v, bool y_bf16) {
 // What bounds the large tile, 4096 x 8192 -> 29568 without corrections, in a long loop (us; 1.98e12
 // operations): 498 in 4 x 2 waves (64 x 128 channels each), 505 in 2 x 4, 508 in 2 x 2 of 128 x 128; without
 // the stores of y 451, without the copies' traffic 450, without both 429; the same products on registers
-// alone 300 (6.6 POP/s: the clock falls with the power that they draw).  Tiles in turn in resident
+// alone 300 (6.6 POP/s).  The clock is 1.77 GHz in both; the matrix cores are busy 52 % of the cycles here and
+// 92 % there, and the waves wait in 28 % of theirs (LDS bank conflicts: none).  Tiles in turn in resident
 // workgroups, the next one's first copies behind the stores of the last, took out the stalls between tiles
 // but no time.  With both corrections 535, into bf16 500.
 template <int BM, int BN, int WM, int WN, bool TA, int NS>

@@ -7,8 +7,9 @@
 //   codes of xn / smooth: per-token integers (a_bits 6, 8: as qe_quant_act makes them from xn) or
 //   microscaled 4-bit blocks (a_bits 4: as qe_mx4_quant makes them from xn)
 //
-// The sum is kept in 64 bits because the codes are decided at rounding borders: with it the factor
-// r is the correctly rounded one, so xn and its codes do not depend on the order of the additions.
+// The sum is kept in 64 bits because the codes are decided at rounding borders: of at most 32768 exact squares
+// it is off by less than 2^-37 relative in any order of the additions, so r is the correctly rounded factor
+// unless the exact one lies that close to a border between two float32 values.
 //
 // A workgroup takes rows in turn and its threads the same channels of each: the norm weight, the
 // smoothing factors and their reciprocals stay in registers, the next row is requested before the current
