@@ -141,8 +141,8 @@ struct Mx4Gemm {
     const int32_t* perm;       // [T] or NULL
     float* y;                  // [T][d_out] (bf16 elements when y_bf16)
     float* part;               // [ksplit][T][d_out] when ksplit > 1
-    uint8_t* a_tiled;          // the activations' tiles (mx4_tiled plans): made from codes and scales when those
-    uint32_t* a_scale;         // are given, else already there, in the order of perm
+    uint8_t* a_tiled;          // the activations' tiles (128- and 256-token tiles), in the order of perm: made
+    uint32_t* a_scale;         // from codes and scales when those are given, else already there
     int T, d_in, d_out, rs_pad, rr_pad, n_r;
     bool y_bf16;
 };
