@@ -55,7 +55,7 @@ typedef enum {
     QE_ERR_HIP = 5           /* a HIP call failed; see qe_last_hip_error() */
 } qe_status;
 
-typedef enum { QE_F32 = 0, QE_BF16 = 1 } qe_dtype;
+typedef enum { QE_F32 = 0, QE_BF16 = 1, QE_I8 = 2 } qe_dtype; /* QE_I8: key/value caches only */
 
 /* Shape and bit widths of one QE linear, plus its prepared parameter buffer.
  *   d_in, d_out  input / output channels (d_in > 0, d_out > 0)
@@ -372,6 +372,133 @@ int qe_mx4_gemm(const qe_linear* lin, const uint8_t* codes, const uint8_t* scale
 int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* weight, int32_t weight_dtype,
                    float eps, int32_t T, int32_t d, void* h, void* xn, const float* smooth, int32_t a_bits, void* codes,
                    void* scales, void* stream);
+
+/* ------------------------------------- rotary positions, paged cache, attention --
+ * What a decoder layer does between its q/k/v linears and its o linear, for prompts, for single tokens and for trees
+ * of drafted tokens, and the choice among the drafts after the last layer.
+ *
+ * Rotary positions (Su et al., "RoFormer"): the first rot_dim channels of a head are rot_dim / 2 pairs, and pair i of a
+ * token at position pos turns by the angle pos * inv_freq[i]:
+ *   c = float32(scale cos(angle)), s = float32(scale sin(angle)), the angle and both functions in float64
+ *   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), products and sums in float32
+ *   rot_dim   a multiple of 16, at most the head's channels; the channels past it are kept
+ *   layout    QE_ROPE_HALF: pair i is the channels i and i + rot_dim / 2; QE_ROPE_PAIRS: 2i and 2i + 1
+ *   n_pos     rows of positions: 1, or 3 (image and video tokens: time, row, column), of which the first sections[0]
+ *             pairs take row 0, the next sections[1] row 1 and the other sections[2] row 2 (their sum: rot_dim / 2;
+ *             ignored for 1)
+ *   scale     factor of cosines and sines (1 unless the frequencies were scaled by QE_ROPE_YARN), finite and > 0
+ *   inv_freq  device float64 [rot_dim / 2], radians per position
+ * Positions: device int32 [n_pos][T].
+ *
+ * qe_rope_freqs (host): inv_freq_host[i] = base^(-2i / rot_dim), scaled for contexts `factor` times longer than trained:
+ *   QE_ROPE_PLAIN  not at all
+ *   QE_ROPE_LINEAR divided by factor (position interpolation)
+ *   QE_ROPE_NTK    with base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   QE_ROPE_YARN   Peng et al., "YaRN", section 3.2: with r = trained_len * inv_freq / (2 pi) turns over the trained
+ *                  context and g = clamp((r - slow) / (fast - slow), 0, 1): inv_freq * (g + (1 - g) / factor)
+ *   *scale_host = 1, for QE_ROPE_YARN 0.1 ln(factor) + 1.  base > 1, factor >= 1, and for QE_ROPE_YARN trained_len > 0
+ *   and fast > slow; the others ignore these three.  rot_dim >= 16 as above (any even number with QE_ROPE_PLAIN or
+ *   QE_ROPE_LINEAR would do; the kernels' limit is checked here).
+ * qe_rope_apply: y = the n_heads heads of x turned.  x: device [T][n_heads][head_dim] of x_dtype, tokens x_stride
+ *   elements apart; y: the same of y_dtype and y_stride, x itself (then the types and strides are equal) or no overlap.
+ *
+ * A paged cache: n_pages pages of page_size places (a power of two, at most 1024) for n_kv_heads heads of head_dim
+ * channels.  Place p of a cache is place p % page_size of page p / page_size.
+ *   k, v              device [n_pages][n_kv_heads][page_size][head_dim]: bf16 (QE_BF16), or int8 codes (QE_I8)
+ *   k_scale, v_scale  device float32 [n_pages][n_kv_heads][page_size], QE_I8 only (else NULL): a code stands for
+ *                     code * scale
+ * qe_kv_append: token t's keys (turned by rope unless it is NULL) and values go to place slot[t]; slot entries below 0
+ *   or past the last place are skipped; the places of a call differ (of two tokens with one place either may
+ *   end up there, or parts of both).  QE_BF16: rounded to nearest even; QE_I8: scale = max |x| / 127 over the head,
+ *   codes as qe_quant_act's (zero heads: scale 0).  k, v: device [T][n_kv_heads][head_dim] of x_dtype, tokens
+ *   k_stride and v_stride elements apart.  With n_heads > 0 the queries are turned in the same launch: q and q_out
+ *   device [T][n_heads][head_dim], as qe_rope_apply's x and y (a copy where rope is NULL).
+ * head_dim: a multiple of 16, at most 256.  Strides: multiples of 8, at least heads * head_dim.  At most 4096 heads.
+ *
+ * qe_attention: for every sequence s, its new tokens t = q_start[s] + i (i < n = q_start[s + 1] - q_start[s]) over its
+ *   kv_len[s] keys, the last n of which are the new tokens' own (qe_kv_append comes first):
+ *     out[t][h] = sum_j softmax_j(scale q[t][h] . K[j]) V[j],  with key head h / (n_heads / n_kv_heads)
+ *   over the keys j that t sees: every key before the new tokens, and of those
+ *     tree NULL   its own and the ones before it
+ *     tree        the i'-th where bit i' % 32 of tree[t][i' / 32] is set (its ancestors and itself); tree device
+ *                 uint32 [T][tree_words], words past tree_words are zeros
+ *   A token that sees no key gets zeros.
+ *   q, out: device bf16 [T][n_heads][head_dim], tokens q_stride and out_stride elements apart; no overlap.
+ *   q_start: device int32 [n_seq + 1], ascending from 0 on, at most T; rows of out behind the last sequence are left as
+ *   they were.  kv_len: device int32 [n_seq].  pages: device int32 [n_seq][max_pages], entry p the page of the
+ *   sequence's keys p * page_size and on.  max_q, max_kv: no sequence has more new tokens or keys (what exceeds them
+ *   is left out); they choose the launch, so that a captured call serves every length up to them.
+ *   Lengths past max_pages * page_size are cut to it, keys of pages outside the cache are not seen, and what lies in
+ *   places past kv_len is not read, so it may be anything; keys and values before that are finite.
+ *   Products on the matrix cores with float32 sums, maxima and sums of the softmax in float32, its weights rounded to
+ *   bf16 (QE_I8: after their values' scales) for the second product.  Deterministic.
+ *   head_dim 64 or 128 (else QE_ERR_UNSUPPORTED), n_heads a multiple of n_kv_heads, max_kv at most 2^30, scale > 0.
+ *   ws: device, qe_attention_workspace_bytes bytes (0 for many calls; 0 too for refused arguments), not shared by calls
+ *   that overlap.
+ *
+ * qe_verify_drafts: how many drafted tokens of every sequence stand, and the token after them.  Sequence s has the rows
+ *   row_start[s] .. row_start[s + 1] - 1: row 0 the last accepted token, every other a drafted token.  p: device float32
+ *   [n_rows][vocab], the target's probabilities after each row; token: device int32 [n_rows] (row 0's is not read);
+ *   u: device float32 [n_rows] in [0, 1), row i's for its acceptance and row 0's for the draw at the end.
+ *   Chain with the drafts' distributions (draft_p device float32 [n_rows][vocab], row i the one token i was drawn from;
+ *     parent NULL): row i is accepted while u[i] draft_p[i][token[i]] < p[i - 1][token[i]].  After the first row that
+ *     is not, the next token is drawn from max(p[i - 1] - draft_p[i], 0); after the last row from its p.
+ *   Chosen tokens (draft_p NULL): parent device int32 [n_rows], the row below row i (< i) that it follows, or NULL for a
+ *     chain.  From row 0 on: the current row c's children in ascending order, child i accepted if u[i] rest < p[c][token[i]],
+ *     with rest = 1 - the p[c] of the children refused before it (a token refused there before is refused again); an
+ *     accepted child becomes the current row.  Where none is accepted, the next token is drawn from p[c] without the
+ *     refused tokens.
+ *   The draw takes the smallest j whose weights' sum up to j exceeds u[0] times the sum of all; where the weights sum to
+ *   nothing it draws from the row of p itself, and where that does too, next is -1.
+ *   taken: device int32 [n_seq], how many are accepted; path: device int32 [n_rows], from row_start[s] on the accepted
+ *   rows (numbers within the sequence) in order, -1 behind them; next: device int32 [n_seq].  A sequence without rows:
+ *   taken 0, next -1.  Tokens outside [0, vocab) and rows whose parent is not below them are refused.
+ *   Products, differences and sums in float64.  p_stride, draft_stride: elements from row to row, at least vocab.
+ *   max_rows: no sequence has more rows (at most 1024; what exceeds it is left out); vocab at most 2^22.  Both forms
+ *   at once (draft_p with parent) are QE_ERR_UNSUPPORTED.  ws: qe_verify_workspace_bytes bytes.
+ */
+typedef enum { QE_ROPE_HALF = 0, QE_ROPE_PAIRS = 1 } qe_rope_layout;
+typedef enum { QE_ROPE_PLAIN = 0, QE_ROPE_LINEAR = 1, QE_ROPE_NTK = 2, QE_ROPE_YARN = 3 } qe_rope_scaling;
+
+typedef struct qe_rope {
+    int32_t rot_dim;
+    int32_t layout;
+    int32_t n_pos;
+    int32_t sections[3];
+    float scale;
+    const double* inv_freq;
+} qe_rope;
+
+typedef struct qe_kv_cache {
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t n_pages;
+    int32_t dtype;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+} qe_kv_cache;
+
+int qe_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained_len, double slow,
+                  double fast, double* inv_freq_host, float* scale_host);
+int qe_rope_apply(const qe_rope* rope, const int32_t* pos, const void* x, int32_t x_dtype, int64_t x_stride, int32_t T,
+                  int32_t n_heads, int32_t head_dim, void* y, int32_t y_dtype, int64_t y_stride, void* stream);
+int qe_kv_append(const qe_kv_cache* cache, const void* k, const void* v, int32_t x_dtype, int64_t k_stride,
+                 int64_t v_stride, int32_t T, const int32_t* slot, const qe_rope* rope, const int32_t* pos, const void* q,
+                 int64_t q_stride, int32_t n_heads, void* q_out, int32_t q_out_dtype, int64_t q_out_stride, void* stream);
+size_t qe_attention_workspace_bytes(const qe_kv_cache* cache, int32_t n_heads, int32_t T, int32_t n_seq, int32_t max_q,
+                                    int32_t max_kv);
+int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t T, int32_t n_heads,
+                 const int32_t* q_start, const int32_t* kv_len, const int32_t* pages, int32_t n_seq, int32_t max_pages,
+                 int32_t max_q, int32_t max_kv, const uint32_t* tree, int32_t tree_words, float scale, uint16_t* out,
+                 int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+size_t qe_verify_workspace_bytes(int32_t n_seq, int32_t vocab);
+int qe_verify_drafts(const float* p, int64_t p_stride, const float* draft_p, int64_t draft_stride, int32_t vocab,
+                     const int32_t* row_start, int32_t n_rows, const int32_t* token, const int32_t* parent, const float* u,
+                     int32_t n_seq, int32_t max_rows, int32_t* taken, int32_t* path, int32_t* next, void* ws,
+                     size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------- channel-importance statistic --
  * (a8 helper) w[j] = (sum_i |W[i][j]|) / d_out: the column mean of |W_f|, one value

@@ -18,7 +18,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqe.so")
 
 QE_OK, QE_ERR_INVALID_ARG, QE_ERR_UNSUPPORTED, QE_ERR_ALIGNMENT, QE_ERR_WORKSPACE, QE_ERR_HIP = range(6)
-QE_F32, QE_BF16 = 0, 1
+QE_F32, QE_BF16, QE_I8 = 0, 1, 2
+QE_ROPE_HALF, QE_ROPE_PAIRS = 0, 1
+QE_ROPE_PLAIN, QE_ROPE_LINEAR, QE_ROPE_NTK, QE_ROPE_YARN = range(4)
 
 
 class QEError(RuntimeError):
@@ -44,6 +46,31 @@ class qe_linear(ctypes.Structure):
     ]
 
 
+class qe_rope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("n_pos", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 3),
+        ("scale", ctypes.c_float),
+        ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class qe_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -51,7 +78,8 @@ def _load():
             "(hipcc, gfx950). There is no fallback implementation.")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z, D = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.POINTER(ctypes.c_double)
-    LP = ctypes.POINTER(qe_linear)
+    LP, RP, CP = ctypes.POINTER(qe_linear), ctypes.POINTER(qe_rope), ctypes.POINTER(qe_kv_cache)
+    Q, F, G = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     sig = {
         "qe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "qe_last_hip_error": (ctypes.c_int, []),
@@ -77,6 +105,13 @@ def _load():
         "qe_mx4_prepare": (ctypes.c_int, [LP, P, P, P, P, P, P, P, P, P, P]),
         "qe_mx4_gemm": (ctypes.c_int, [LP, P, P, I, P, P, P, P, P, P, Z, P]),
         "qe_add_rmsnorm": (ctypes.c_int, [P, P, I, P, I, ctypes.c_float, I, I, P, P, P, I, P, P, P]),
+        "qe_rope_freqs": (ctypes.c_int, [I, G, I, G, G, G, G, P, P]),
+        "qe_rope_apply": (ctypes.c_int, [RP, P, P, I, Q, I, I, I, P, I, Q, P]),
+        "qe_kv_append": (ctypes.c_int, [CP, P, P, I, Q, Q, I, P, RP, P, P, Q, I, P, I, Q, P]),
+        "qe_attention_workspace_bytes": (Z, [CP, I, I, I, I, I]),
+        "qe_attention": (ctypes.c_int, [CP, P, Q, I, I, P, P, P, I, I, I, I, P, I, F, P, Q, P, Z, P]),
+        "qe_verify_workspace_bytes": (Z, [I, I]),
+        "qe_verify_drafts": (ctypes.c_int, [P, Q, P, Q, I, P, I, P, P, P, I, I, P, P, P, P, Z, P]),
         "qe_colmean_abs": (ctypes.c_int, [P, I, I, I, P, P]),
         "qe_channel_topk": (ctypes.c_int, [P, I, P, I, I, I, P, P, P]),
         "qe_partition_channels": (ctypes.c_int, [P, I, I, I, P, P, P]),
@@ -128,6 +163,8 @@ EXPORTED = (
     "qe_build_experts", "qe_lowrank_cov_workspace_bytes", "qe_lowrank_fit_cov",
     "qe_build_experts_cov_workspace_bytes", "qe_build_experts_cov", "qe_router_targets_workspace_bytes", "qe_router_targets", "qe_router_fit_workspace_bytes",
     "qe_router_fit", "qe_mx4_quant", "qe_mx4_dequant", "qe_mx4_prepare", "qe_mx4_gemm", "qe_add_rmsnorm",
+    "qe_rope_freqs", "qe_rope_apply", "qe_kv_append", "qe_attention_workspace_bytes", "qe_attention",
+    "qe_verify_workspace_bytes", "qe_verify_drafts",
 )
 
 
@@ -394,6 +431,152 @@ def qe_add_rmsnorm(x, res, weight, eps, h=None, xn=None, smooth=None, a_bits=0, 
     pe = _arg(f, "scales", scales, (T, d // 32) if mx else (T,), torch.uint8 if mx else torch.float32, dev)
     _call_on(dev, f, _lib.qe_add_rmsnorm, px, pr, _dtype_code(x), pw, _dtype_code(weight), eps, T, d, ph, pn, ps, a_bits,
              pc, pe, stream=stream)
+
+
+def make_rope(inv_freq, pairs=False, sections=None, scale=1.0) -> qe_rope:
+    """Rotation of a head's first 2 * len(inv_freq) channels (inv_freq: device float64, kept by the result); pairs:
+    neighbouring channels turn together, else the halves'; sections: how many pairs take each of three position rows."""
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("make_rope: inv_freq must be a dense float64 vector")
+    s = tuple(sections) if sections is not None else (0, 0, 0)
+    if len(s) != 3:
+        raise ValueError("make_rope: sections are three")
+    r = qe_rope(2 * inv_freq.shape[0], QE_ROPE_PAIRS if pairs else QE_ROPE_HALF, 1 if sections is None else 3,
+                (ctypes.c_int32 * 3)(*s), scale, inv_freq.data_ptr())
+    r.tensor = inv_freq
+    return r
+
+
+def make_cache(k, v, k_scale=None, v_scale=None) -> qe_kv_cache:
+    """The paged cache in k and v [n_pages, n_kv_heads, page_size, head_dim] (bf16, or int8 with float32 scales of that
+    shape without the channels); the result keeps the tensors."""
+    if k.dim() != 4:
+        raise ValueError("make_cache: k must have shape (n_pages, n_kv_heads, page_size, head_dim)")
+    if k.dtype not in (torch.bfloat16, torch.int8):
+        raise TypeError(f"make_cache: caches are bf16 or int8, got {k.dtype}")
+    i8, dev = k.dtype is torch.int8, k.get_device()
+    if i8 != (k_scale is not None) or i8 != (v_scale is not None):
+        raise ValueError("make_cache: int8 caches have scales, bf16 caches have none")
+    p = [_arg("make_cache", name, t, shape, dtype, dev) for name, t, shape, dtype in (
+        ("k", k, k.shape, k.dtype), ("v", v, k.shape, k.dtype), ("k_scale", k_scale, k.shape[:3], torch.float32),
+        ("v_scale", v_scale, k.shape[:3], torch.float32))]
+    n, h, s, d = k.shape
+    c = qe_kv_cache(h, d, s, n, QE_I8 if i8 else QE_BF16, *p)
+    c.tensors, c.device_index = (k, v, k_scale, v_scale), dev
+    return c
+
+
+def _rows(where, name, t, shape, index):
+    """Address and token stride of heads [T, heads, head_dim] on device `index` (dense but for the tokens)."""
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{where}: {name} is on {t.device}, not on device {index}")
+    T, h, d = shape
+    st = t.stride()
+    if d > 1 and st[2] != 1 or h > 1 and st[1] != d:
+        raise ValueError(f"{where}: {name} must be dense within a token")
+    return t.data_ptr(), st[0] if T > 1 else h * d
+
+
+def _pos(where, rope, pos, T, index):
+    return _arg(where, "pos", pos, (T,) if rope.n_pos == 1 and pos is not None and pos.dim() == 1 else (rope.n_pos, T),
+                torch.int32, index)
+
+
+def qe_rope_freqs(rot_dim, base, scaling=QE_ROPE_PLAIN, factor=1.0, trained_len=0.0, slow=1.0, fast=32.0):
+    """Host inverse frequencies (float64 ndarray [rot_dim / 2]) and the factor of cosines and sines."""
+    f, s = np.empty(max(rot_dim, 0) // 2, np.float64), ctypes.c_float()
+    _check(_lib.qe_rope_freqs(rot_dim, base, scaling, factor, trained_len, slow, fast, _ptr(f), ctypes.byref(s)),
+           "qe_rope_freqs")
+    return f, s.value
+
+
+def qe_rope_apply(rope: qe_rope, pos, x, y, stream=None):
+    """Enqueue y = x [T, heads, head_dim] turned by the positions pos (int32 [n_pos, T], or [T]); y may be x."""
+    f, dev, (T, h, d) = "qe_rope_apply", x.get_device(), x.shape
+    px, sx = _rows(f, "x", x, x.shape, dev)
+    py, sy = _rows(f, "y", y, x.shape, dev)
+    pp = _pos(f, rope, pos, T, dev)
+    _call_on(dev, f, _lib.qe_rope_apply, ctypes.byref(rope), pp, px, _dtype_code(x), sx, T, h, d, py, _dtype_code(y), sy,
+             stream=stream)
+
+
+def qe_kv_append(cache: qe_kv_cache, k, v, slot, rope=None, pos=None, q=None, q_out=None, stream=None):
+    """Enqueue: keys (turned by rope at pos) and values [T, n_kv_heads, head_dim] go to the places slot (int32 [T],
+    below 0: skipped); q [T, heads, head_dim] is turned into q_out in the same launch."""
+    f, dev, T, d = "qe_kv_append", cache.device_index, k.shape[0], cache.head_dim
+    shape = (T, cache.n_kv_heads, d)
+    pk, sk = _rows(f, "k", k, shape, dev)
+    pv, sv = _rows(f, "v", v, shape, dev)
+    ps = _arg(f, "slot", slot, (T,), torch.int32, dev)
+    pp = None if rope is None else _pos(f, rope, pos, T, dev)
+    if v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
+        raise TypeError(f"{f}: q, k and v must have one type")
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{f}: q and q_out come together")
+    pq = po = None
+    sq = so = h = od = 0
+    if q is not None:
+        h = q.shape[1]
+        pq, sq = _rows(f, "q", q, (T, h, d), dev)
+        po, so = _rows(f, "q_out", q_out, (T, h, d), dev)
+        od = _dtype_code(q_out)
+    _call_on(dev, f, _lib.qe_kv_append, ctypes.byref(cache), pk, pv, _dtype_code(k), sk, sv, T, ps,
+             None if rope is None else ctypes.byref(rope), pp, pq, sq, h, po, od, so, stream=stream)
+
+
+def qe_attention_workspace_bytes(cache: qe_kv_cache, n_heads, T, n_seq, max_q, max_kv) -> int:
+    return _lib.qe_attention_workspace_bytes(ctypes.byref(cache), n_heads, T, n_seq, max_q, max_kv)
+
+
+def qe_attention(cache: qe_kv_cache, q, q_start, kv_len, pages, max_q, max_kv, out, ws, tree=None, scale=None, stream=None):
+    """Enqueue the attention of the new tokens q (bf16 [T, heads, head_dim]) over the cache (see include/qe.h); tree:
+    int32 or uint32 bits [T, words]; scale: 1 / sqrt(head_dim) where left out; ws: a byte tensor, or None for no bytes."""
+    f, dev, (T, h, d) = "qe_attention", cache.device_index, q.shape
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16:
+        raise TypeError(f"{f}: q and out must be bf16")
+    if d != cache.head_dim:
+        raise ValueError(f"{f}: q has heads of {d} channels, the cache of {cache.head_dim}")
+    pq, sq = _rows(f, "q", q, q.shape, dev)
+    po, so = _rows(f, "out", out, q.shape, dev)
+    n = kv_len.shape[0]
+    p0 = _arg(f, "q_start", q_start, (n + 1,), torch.int32, dev)
+    pl = _arg(f, "kv_len", kv_len, (n,), torch.int32, dev)
+    pp = _arg(f, "pages", pages, (n, pages.shape[-1]), torch.int32, dev)
+    words = 0 if tree is None else tree.shape[-1]
+    pt = None if tree is None else _arg(f, "tree", tree, (T, words),
+                                        torch.uint32 if tree.dtype is torch.uint32 else torch.int32, dev)
+    pw = None if ws is None else _arg(f, "ws", ws, ws.shape, ws.dtype, dev)
+    _call_on(dev, f, _lib.qe_attention, ctypes.byref(cache), pq, sq, T, h, p0, pl, pp, n, pages.shape[-1], max_q, max_kv,
+             pt, words, d ** -0.5 if scale is None else scale, po, so, pw, 0 if ws is None else ws.nbytes, stream=stream)
+
+
+def qe_verify_workspace_bytes(n_seq, vocab) -> int:
+    return _lib.qe_verify_workspace_bytes(n_seq, vocab)
+
+
+def qe_verify_drafts(p, row_start, token, u, taken, path, next, ws, draft_p=None, parent=None, max_rows=1024, stream=None):
+    """Enqueue the verification of drafted tokens (see include/qe.h): p and draft_p float32 [n_rows, vocab], dense
+    within a row; draft_p for chains drawn from it, parent (int32 [n_rows]) for trees of chosen tokens."""
+    f, dev, (N, V), n = "qe_verify_drafts", p.get_device(), p.shape, taken.shape[0]
+    strides = []
+    for name, t in (("p", p), ("draft_p", draft_p)):
+        if t is None:
+            strides.append(V)
+            continue
+        if t.dtype is not torch.float32:
+            raise TypeError(f"{f}: {name} must be float32, got {t.dtype}")
+        if t.shape != (N, V) or t.get_device() != dev or (V > 1 and t.stride(1) != 1):
+            raise ValueError(f"{f}: {name} must have shape {(N, V)} on device {dev}, dense within a row")
+        strides.append(t.stride(0) if N > 1 else V)
+    i32 = torch.int32
+    a = [_arg(f, name, t, shape, dtype, dev) for name, t, shape, dtype in (
+        ("row_start", row_start, (n + 1,), i32), ("token", token, (N,), i32), ("parent", parent, (N,), i32),
+        ("u", u, (N,), torch.float32), ("taken", taken, (n,), i32), ("path", path, (N,), i32), ("next", next, (n,), i32),
+        ("ws", ws, ws.shape, ws.dtype))]
+    _call_on(dev, f, _lib.qe_verify_drafts, p.data_ptr(), strides[0], _ptr(draft_p), strides[1], V, a[0], N, a[1], a[2],
+             a[3], n, max_rows, a[4], a[5], a[6], a[7], ws.nbytes, stream=stream)
 
 
 def qe_colmean_abs(W, w, stream=None):

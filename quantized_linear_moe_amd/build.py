@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqe.so")
 SOURCES = ["qe_api.hip", "k_act.hip", "k_gemm_w4.hip", "k_decode.hip", "k_stat.hip", "k_prep.hip", "k_probe.hip",
-           "k_cooc.hip", "calib_host.hip", "k_gemm_a16.hip", "k_lowrank.hip", "k_norm.hip", "k_mx4.hip", "k_gemm_mx4.hip"]
+           "k_cooc.hip", "calib_host.hip", "k_gemm_a16.hip", "k_lowrank.hip", "k_norm.hip", "k_mx4.hip", "k_gemm_mx4.hip",
+           "k_rope.hip", "k_attn.hip", "k_verify.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,225 @@
+// Rotary positions of query heads, and keys and values appended to the paged cache with the keys rotated on the way.
+//
+//   a = pos * inv_freq[i] (float64);  c = float32(scale cos a), s = float32(scale sin a)
+//   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s) in float32, one rounding to the output's type
+//   8-bit cache: scale = max |x'| / 127 over the head, codes as qe_quant_act makes them
+//
+// Angles of far positions lose their fraction in 32 bits (10^6 radians: a step of 0.06), so the angle and its sine and
+// cosine are taken in 64 bits, once per token and pair for all its heads, into LDS.  A workgroup takes one token (few
+// heads: several); a lane takes 16 channels of a head as two vectors of 8, whose pairs both lie in the lane.
+#include <algorithm>
+
+#include "qe_act.h"
+#include "qe_cache.h"
+#include "qe_mx4.h"
+
+namespace qe {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 16;  // tokens of a workgroup at most
+
+struct RopeArgs {
+    const void* x[3];
+    int64_t x_stride[3];
+    int heads[3];
+    int T, head_dim, tokens;  // tokens of a workgroup
+    int lanes, lane_shift;    // lanes of a head: the power of two at or above head_dim / 16
+    int rot, layout, n_pos, sec0, sec1;
+    double scale;
+    const double* inv_freq;
+    const int32_t* pos;
+    void* q_out;
+    int64_t q_out_stride;
+    int q_out_bf16;
+    void* cache[2];
+    float* cache_scale[2];
+    int i8, page_shift;
+    uint32_t slots;
+    const int32_t* slot;
+};
+
+__device__ inline void store8_as(void* p, size_t idx, const float v[8], bool bf16) {
+    if (bf16) {
+        v4u o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = mx4_bf16_bits(v[2 * i]) | (mx4_bf16_bits(v[2 * i + 1]) << 16);
+        *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(p) + idx) = o;
+    } else {
+        v4f* q = reinterpret_cast<v4f*>(reinterpret_cast<float*>(p) + idx);
+        q[0] = v4f{v[0], v[1], v[2], v[3]};
+        q[1] = v4f{v[4], v[5], v[6], v[7]};
+    }
+}
+
+// A lane's 16 channels of one head: which they are, and their values
+struct Item {
+    int part, head, ch0, ch1;  // part 0 q, 1 k, 2 v; -1: none
+    long t;
+    bool turn;
+    int pair0;
+    float a[8], b[8];
+};
+
+template <bool kBf16>
+__device__ inline void load_item(const RopeArgs& A, int item, int n_items, long t0, Item& I) {
+    const int per_token = (A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift;
+    const int tok = item / per_token, rest = item - tok * per_token;
+    int head = rest >> A.lane_shift;
+    const int lane = rest & (A.lanes - 1);
+    I.t = t0 + tok;
+    I.part = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) I.a[i] = I.b[i] = 0.0f;
+    if (item >= n_items || I.t >= A.T || lane * 16 >= A.head_dim) return;
+    int part = 0;
+    if (head >= A.heads[0]) {
+        head -= A.heads[0];
+        part = 1;
+        if (head >= A.heads[1]) {
+            head -= A.heads[1];
+            part = 2;
+        }
+    }
+    I.part = part;
+    I.head = head;
+    I.turn = part < 2 && lane * 16 < A.rot;
+    I.pair0 = 8 * lane;
+    const bool halves = I.turn && A.layout == QE_ROPE_HALF;
+    I.ch0 = halves ? 8 * lane : 16 * lane;
+    I.ch1 = halves ? A.rot / 2 + 8 * lane : 16 * lane + 8;
+    const void* x = part == 0 ? A.x[0] : part == 1 ? A.x[1] : A.x[2];
+    const int64_t stride = part == 0 ? A.x_stride[0] : part == 1 ? A.x_stride[1] : A.x_stride[2];
+    const size_t at = (size_t)I.t * stride + (size_t)head * A.head_dim;
+    load8(x, kBf16 ? QE_BF16 : QE_F32, at + I.ch0, I.a);
+    load8(x, kBf16 ? QE_BF16 : QE_F32, at + I.ch1, I.b);
+}
+
+__device__ inline void turn_item(const RopeArgs& A, const float2 (*cs)[kMaxHeadDim / 2], long t0, Item& I) {
+    const float2* p = cs[I.t - t0] + I.pair0;
+    if (A.layout == QE_ROPE_HALF) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = p[i].x, s = p[i].y, x1 = I.a[i], x2 = I.b[i];
+            I.a[i] = x1 * c - x2 * s;
+            I.b[i] = x2 * c + x1 * s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = p[i].x, s = p[i].y, x1 = I.a[2 * i], x2 = I.a[2 * i + 1];
+            I.a[2 * i] = x1 * c - x2 * s;
+            I.a[2 * i + 1] = x2 * c + x1 * s;
+            const float c2 = p[4 + i].x, s2 = p[4 + i].y, y1 = I.b[2 * i], y2 = I.b[2 * i + 1];
+            I.b[2 * i] = y1 * c2 - y2 * s2;
+            I.b[2 * i + 1] = y2 * c2 + y1 * s2;
+        }
+    }
+}
+
+// (every lane of the wave calls it: the 8-bit form takes the largest value over a head's lanes)
+__device__ inline void store_item(const RopeArgs& A, const Item& I) {
+    if (I.part == 0) {
+        const size_t at = (size_t)I.t * A.q_out_stride + (size_t)I.head * A.head_dim;
+        store8_as(A.q_out, at + I.ch0, I.a, A.q_out_bf16);
+        store8_as(A.q_out, at + I.ch1, I.b, A.q_out_bf16);
+    }
+    float sx = 0.0f;
+    if (A.i8) {
+        float m = fmaxf(absmax8(I.a), absmax8(I.b));
+        for (int off = A.lanes >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+        sx = m / 127.0f;
+    }
+    if (I.part < 1) return;
+    const uint32_t slot = (uint32_t)A.slot[I.t];
+    if (slot >= A.slots) return;  // (negative: padding)
+    const int c = I.part - 1;
+    const int heads = c ? A.heads[2] : A.heads[1];
+    const size_t row = ((((size_t)(slot >> A.page_shift) * heads + I.head) << A.page_shift)) +
+                       (slot & ((1u << A.page_shift) - 1));
+    void* dst = c ? A.cache[1] : A.cache[0];
+    if (A.i8) {
+        uint8_t* o = reinterpret_cast<uint8_t*>(dst) + row * A.head_dim;
+        *reinterpret_cast<v2u*>(o + I.ch0) = quant8(I.a, sx, 127.0f);
+        *reinterpret_cast<v2u*>(o + I.ch1) = quant8(I.b, sx, 127.0f);
+        if (I.pair0 == 0) (c ? A.cache_scale[1] : A.cache_scale[0])[row] = sx;
+    } else {
+        store8_as(dst, row * A.head_dim + I.ch0, I.a, true);
+        store8_as(dst, row * A.head_dim + I.ch1, I.b, true);
+    }
+}
+
+template <bool kBf16>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A) {
+    __shared__ float2 cs[kRopeTokens][kMaxHeadDim / 2];
+    const long t0 = (long)blockIdx.x * A.tokens;
+    const int n_items = A.tokens * ((A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift);
+    const int wave0 = threadIdx.x & ~(kWave - 1);
+    Item now, next;
+    load_item<kBf16>(A, threadIdx.x, n_items, t0, now);  // (requested before the angles are worked out)
+    if (A.rot > 0) {
+        const int pairs = A.rot / 2;
+        for (int i = threadIdx.x; i < A.tokens * pairs; i += kRopeThreads) {
+            const int tok = i / pairs, p = i - tok * pairs;
+            if (t0 + tok >= A.T) break;
+            const int row = A.n_pos == 1 ? 0 : p < A.sec0 ? 0 : p < A.sec0 + A.sec1 ? 1 : 2;
+            double s, c;
+            sincos((double)A.pos[(size_t)row * A.T + t0 + tok] * A.inv_freq[p], &s, &c);
+            cs[tok][p] = make_float2((float)(c * A.scale), (float)(s * A.scale));
+        }
+    }
+    __syncthreads();
+    for (int base = 0; base + wave0 < n_items; base += kRopeThreads) {
+        load_item<kBf16>(A, base + kRopeThreads + (int)threadIdx.x, n_items, t0, next);
+        if (now.part >= 0 && now.turn) turn_item(A, cs, t0, now);
+        store_item(A, now);
+        now = next;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeLaunch& R, hipStream_t st) {
+    RopeArgs A = {};
+    for (int i = 0; i < 3; ++i) {
+        A.x[i] = R.x[i];
+        A.x_stride[i] = R.x_stride[i];
+        A.heads[i] = R.x[i] ? R.heads[i] : 0;
+    }
+    A.T = R.T;
+    A.head_dim = R.head_dim;
+    while (16 << A.lane_shift < R.head_dim) ++A.lane_shift;
+    A.lanes = 1 << A.lane_shift;
+    const long per_token = (long)(A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift;
+    A.tokens = (int)std::max<long>(1, std::min<long>(kRopeTokens, kRopeThreads / per_token));
+    if (R.rope) {
+        A.rot = R.rope->rot_dim;
+        A.layout = R.rope->layout;
+        A.n_pos = R.rope->n_pos;
+        A.sec0 = R.rope->sections[0];
+        A.sec1 = R.rope->sections[1];
+        A.scale = (double)R.rope->scale;
+        A.inv_freq = R.rope->inv_freq;
+    }
+    A.pos = R.pos;
+    A.q_out = R.q_out;
+    A.q_out_stride = R.q_out_stride;
+    A.q_out_bf16 = R.q_out_bf16;
+    if (R.cache) {
+        A.cache[0] = R.cache->k;
+        A.cache[1] = R.cache->v;
+        A.cache_scale[0] = R.cache->k_scale;
+        A.cache_scale[1] = R.cache->v_scale;
+        A.i8 = R.cache->dtype == QE_I8;
+        while (1 << A.page_shift < R.cache->page_size) ++A.page_shift;
+        A.slots = (uint32_t)R.cache->n_pages * (uint32_t)R.cache->page_size;
+        A.slot = R.slot;
+    }
+    const dim3 grid((unsigned)((R.T + A.tokens - 1) / A.tokens));
+    if (R.x_bf16) hipLaunchKernelGGL(rope_kernel<true>, grid, dim3(kRopeThreads), 0, st, A);
+    else hipLaunchKernelGGL(rope_kernel<false>, grid, dim3(kRopeThreads), 0, st, A);
+    return hipGetLastError();
+}
+
+}  // namespace qe

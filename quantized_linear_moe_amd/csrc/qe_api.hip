@@ -10,6 +10,7 @@
 #include <thread>
 #include <vector>
 
+#include "qe_cache.h"
 #include "qe_calib.h"
 #include "qe_lowrank.h"
 #include "qe_internal.h"
@@ -679,6 +680,256 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
         QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
     QE_TRY_HIP(launch_add_rmsnorm(x, res, x_dtype, weight, weight_dtype, eps, T, d, h, xn, smooth, a_bits,
                                   static_cast<uint8_t*>(codes), scales, S(stream)));
+    return QE_OK;
+}
+
+// ------------------------------------- rotary positions, paged cache, attention, drafts
+namespace {
+
+int validate_rope(const qe_rope* r, int32_t head_dim) {
+    QE_CHECK(r != nullptr, QE_ERR_INVALID_ARG);
+    QE_CHECK(r->rot_dim > 0 && r->rot_dim <= head_dim, QE_ERR_INVALID_ARG);
+    QE_CHECK(r->layout == QE_ROPE_HALF || r->layout == QE_ROPE_PAIRS, QE_ERR_INVALID_ARG);
+    QE_CHECK(r->n_pos == 1 || r->n_pos == 3, QE_ERR_INVALID_ARG);
+    if (r->n_pos == 3) {
+        for (int s : r->sections) QE_CHECK(s >= 0 && s <= r->rot_dim, QE_ERR_INVALID_ARG);
+        QE_CHECK(2 * (r->sections[0] + r->sections[1] + r->sections[2]) == r->rot_dim, QE_ERR_INVALID_ARG);
+    }
+    QE_CHECK(r->scale > 0.0f && r->scale <= 3.402823466e38f, QE_ERR_INVALID_ARG);
+    QE_CHECK(r->rot_dim % 16 == 0, QE_ERR_UNSUPPORTED);
+    QE_CHECK(r->inv_freq != nullptr, QE_ERR_INVALID_ARG);
+    QE_CHECK(aligned16(r->inv_freq), QE_ERR_ALIGNMENT);
+    return QE_OK;
+}
+
+int validate_heads(int32_t n_heads, int32_t head_dim) {
+    QE_CHECK(n_heads > 0 && head_dim > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(n_heads <= 4096 && head_dim % 16 == 0 && head_dim <= kMaxHeadDim, QE_ERR_UNSUPPORTED);
+    return QE_OK;
+}
+
+int validate_cache(const qe_kv_cache* c) {
+    QE_CHECK(c != nullptr, QE_ERR_INVALID_ARG);
+    int st = validate_heads(c->n_kv_heads, c->head_dim);
+    if (st) return st;
+    QE_CHECK(c->page_size > 0 && c->n_pages > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK((c->page_size & (c->page_size - 1)) == 0 && c->page_size <= 1024, QE_ERR_UNSUPPORTED);
+    QE_CHECK((int64_t)c->n_pages * c->page_size <= INT32_MAX, QE_ERR_UNSUPPORTED);  // places are int32
+    QE_CHECK(c->dtype == QE_BF16 || c->dtype == QE_I8, QE_ERR_INVALID_ARG);
+    QE_CHECK(c->k && c->v, QE_ERR_INVALID_ARG);
+    QE_CHECK(c->dtype == QE_I8 ? c->k_scale && c->v_scale : !c->k_scale && !c->v_scale, QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)c->k, (const void*)c->v, (const void*)c->k_scale, (const void*)c->v_scale})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    return QE_OK;
+}
+
+// tokens' distance: whole vectors, and tokens do not overlap
+int validate_stride(int64_t stride, int32_t n_heads, int32_t head_dim) {
+    QE_CHECK(stride >= (int64_t)n_heads * head_dim, QE_ERR_INVALID_ARG);
+    QE_CHECK(stride % 8 == 0, QE_ERR_ALIGNMENT);
+    return QE_OK;
+}
+
+inline bool real_dtype(int32_t d) { return d == QE_F32 || d == QE_BF16; }
+
+}  // namespace
+
+int qe_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained_len, double slow,
+                  double fast, double* inv_freq_host, float* scale_host) {
+    QE_CHECK(rot_dim > 0 && inv_freq_host && scale_host, QE_ERR_INVALID_ARG);
+    QE_CHECK(base > 1.0 && std::isfinite(base), QE_ERR_INVALID_ARG);
+    QE_CHECK(scaling >= QE_ROPE_PLAIN && scaling <= QE_ROPE_YARN, QE_ERR_INVALID_ARG);
+    if (scaling == QE_ROPE_PLAIN) factor = 1.0;
+    QE_CHECK(factor >= 1.0 && std::isfinite(factor), QE_ERR_INVALID_ARG);
+    if (scaling == QE_ROPE_YARN) {
+        QE_CHECK(trained_len > 0.0 && std::isfinite(trained_len), QE_ERR_INVALID_ARG);
+        QE_CHECK(std::isfinite(slow) && std::isfinite(fast) && fast > slow, QE_ERR_INVALID_ARG);
+    }
+    QE_CHECK(rot_dim % 16 == 0 && rot_dim <= kMaxHeadDim, QE_ERR_UNSUPPORTED);
+    if (scaling == QE_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == QE_ROPE_LINEAR) f /= factor;
+        if (scaling == QE_ROPE_YARN) {
+            const double turns = trained_len * f / 6.283185307179586476925;
+            const double g = std::min(std::max((turns - slow) / (fast - slow), 0.0), 1.0);
+            f *= g + (1.0 - g) / factor;
+        }
+        inv_freq_host[i] = f;
+    }
+    *scale_host = scaling == QE_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return QE_OK;
+}
+
+int qe_rope_apply(const qe_rope* rope, const int32_t* pos, const void* x, int32_t x_dtype, int64_t x_stride, int32_t T,
+                  int32_t n_heads, int32_t head_dim, void* y, int32_t y_dtype, int64_t y_stride, void* stream) {
+    QE_CHECK(T >= 0, QE_ERR_INVALID_ARG);
+    int st = validate_heads(n_heads, head_dim);
+    if (!st) st = validate_rope(rope, head_dim);
+    if (st) return st;
+    QE_CHECK(real_dtype(x_dtype) && real_dtype(y_dtype), QE_ERR_INVALID_ARG);
+    if ((st = validate_stride(x_stride, n_heads, head_dim))) return st;
+    if ((st = validate_stride(y_stride, n_heads, head_dim))) return st;
+    if (T == 0) return QE_OK;
+    QE_CHECK(pos && x && y, QE_ERR_INVALID_ARG);
+    QE_CHECK(x != y || (x_dtype == y_dtype && x_stride == y_stride), QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)pos, x, (const void*)y}) QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    RopeLaunch R = {};
+    R.x[0] = x;
+    R.x_stride[0] = x_stride;
+    R.heads[0] = n_heads;
+    R.x_bf16 = x_dtype == QE_BF16;
+    R.T = T;
+    R.head_dim = head_dim;
+    R.rope = rope;
+    R.pos = pos;
+    R.q_out = y;
+    R.q_out_stride = y_stride;
+    R.q_out_bf16 = y_dtype == QE_BF16;
+    QE_TRY_HIP(launch_rope(R, S(stream)));
+    return QE_OK;
+}
+
+int qe_kv_append(const qe_kv_cache* cache, const void* k, const void* v, int32_t x_dtype, int64_t k_stride,
+                 int64_t v_stride, int32_t T, const int32_t* slot, const qe_rope* rope, const int32_t* pos, const void* q,
+                 int64_t q_stride, int32_t n_heads, void* q_out, int32_t q_out_dtype, int64_t q_out_stride, void* stream) {
+    int st = validate_cache(cache);
+    if (st) return st;
+    QE_CHECK(T >= 0 && n_heads >= 0 && real_dtype(x_dtype), QE_ERR_INVALID_ARG);
+    const int32_t hd = cache->head_dim;
+    if (rope && (st = validate_rope(rope, hd))) return st;
+    if ((st = validate_stride(k_stride, cache->n_kv_heads, hd))) return st;
+    if ((st = validate_stride(v_stride, cache->n_kv_heads, hd))) return st;
+    if (n_heads > 0) {
+        QE_CHECK(real_dtype(q_out_dtype), QE_ERR_INVALID_ARG);
+        if ((st = validate_heads(n_heads, hd))) return st;
+        if ((st = validate_stride(q_stride, n_heads, hd))) return st;
+        if ((st = validate_stride(q_out_stride, n_heads, hd))) return st;
+    } else {
+        QE_CHECK(!q && !q_out, QE_ERR_INVALID_ARG);
+    }
+    if (T == 0) return QE_OK;
+    QE_CHECK(k && v && slot && (!rope || pos), QE_ERR_INVALID_ARG);
+    QE_CHECK(n_heads == 0 || (q && q_out), QE_ERR_INVALID_ARG);
+    QE_CHECK(!q || q != q_out || (x_dtype == q_out_dtype && q_stride == q_out_stride), QE_ERR_INVALID_ARG);
+    for (const void* p : {k, v, (const void*)slot, (const void*)pos, q, (const void*)q_out})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    RopeLaunch R = {};
+    const void* x[3] = {n_heads ? q : nullptr, k, v};
+    const int64_t strides[3] = {q_stride, k_stride, v_stride};
+    const int heads[3] = {n_heads, cache->n_kv_heads, cache->n_kv_heads};
+    for (int i = 0; i < 3; ++i) {
+        R.x[i] = x[i];
+        R.x_stride[i] = strides[i];
+        R.heads[i] = heads[i];
+    }
+    R.x_bf16 = x_dtype == QE_BF16;
+    R.T = T;
+    R.head_dim = hd;
+    R.rope = rope;
+    R.pos = pos;
+    R.q_out = q_out;
+    R.q_out_stride = q_out_stride;
+    R.q_out_bf16 = q_out_dtype == QE_BF16;
+    R.cache = cache;
+    R.slot = slot;
+    QE_TRY_HIP(launch_rope(R, S(stream)));
+    return QE_OK;
+}
+
+static int validate_attention(const qe_kv_cache* cache, int32_t n_heads, int32_t T, int32_t n_seq, int32_t max_q,
+                              int32_t max_kv) {
+    int st = validate_cache(cache);
+    if (st) return st;
+    QE_CHECK(n_heads > 0 && n_heads % cache->n_kv_heads == 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(T >= 0 && n_seq >= 0 && max_q >= 0 && max_kv >= 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(n_heads <= 4096 && (cache->head_dim == 64 || cache->head_dim == 128), QE_ERR_UNSUPPORTED);
+    QE_CHECK(max_kv <= 1 << 30, QE_ERR_UNSUPPORTED);
+    // rows of a sequence and key head, and workgroups, are counted in 31 bits
+    QE_CHECK((int64_t)max_q * n_heads <= 1 << 30 && (int64_t)T * n_heads <= (int64_t)1 << 32, QE_ERR_UNSUPPORTED);
+    return QE_OK;
+}
+
+size_t qe_attention_workspace_bytes(const qe_kv_cache* cache, int32_t n_heads, int32_t T, int32_t n_seq, int32_t max_q,
+                                    int32_t max_kv) {
+    if (validate_attention(cache, n_heads, T, n_seq, max_q, max_kv) || T == 0 || n_seq == 0 || max_q == 0) return 0;
+    return attn_partial_bytes(attn_plan(cache, n_heads, n_seq, max_q, max_kv), cache->head_dim, T, n_heads);
+}
+
+int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t T, int32_t n_heads,
+                 const int32_t* q_start, const int32_t* kv_len, const int32_t* pages, int32_t n_seq, int32_t max_pages,
+                 int32_t max_q, int32_t max_kv, const uint32_t* tree, int32_t tree_words, float scale, uint16_t* out,
+                 int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+    int st = validate_attention(cache, n_heads, T, n_seq, max_q, max_kv);
+    if (st) return st;
+    QE_CHECK(max_pages >= 0 && scale > 0.0f && scale <= 3.402823466e38f, QE_ERR_INVALID_ARG);
+    QE_CHECK(!tree || tree_words > 0, QE_ERR_INVALID_ARG);
+    if ((st = validate_stride(q_stride, n_heads, cache->head_dim))) return st;
+    if ((st = validate_stride(out_stride, n_heads, cache->head_dim))) return st;
+    if (T == 0 || n_seq == 0 || max_q == 0) return QE_OK;
+    QE_CHECK(q && out && q_start && kv_len && (pages || max_pages == 0), QE_ERR_INVALID_ARG);
+    QE_CHECK(q != out, QE_ERR_INVALID_ARG);
+    for (const void* p : {(const void*)q, (const void*)out, (const void*)q_start, (const void*)kv_len, (const void*)pages,
+                          (const void*)tree, (const void*)ws})
+        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    const AttnPlan P = attn_plan(cache, n_heads, n_seq, max_q, max_kv);
+    QE_CHECK((int64_t)cache->n_kv_heads * P.row_tiles * n_seq <= INT32_MAX / P.splits, QE_ERR_UNSUPPORTED);
+    const size_t need = attn_partial_bytes(P, cache->head_dim, T, n_heads);
+    QE_CHECK(ws_bytes >= need && (need == 0 || ws), QE_ERR_WORKSPACE);
+    AttnLaunch A = {};
+    A.cache = cache;
+    A.q = q;
+    A.q_stride = q_stride;
+    A.T = T;
+    A.n_heads = n_heads;
+    A.n_seq = n_seq;
+    A.max_pages = max_pages;
+    A.max_q = max_q;
+    A.max_kv = max_kv;
+    A.q_start = q_start;
+    A.kv_len = kv_len;
+    A.pages = pages;
+    A.tree = tree;
+    A.tree_words = tree_words;
+    A.scale = scale;
+    A.out = out;
+    A.out_stride = out_stride;
+    A.ws = ws;
+    QE_TRY_HIP(launch_attention(A, P, S(stream)));
+    return QE_OK;
+}
+
+static int validate_verify(int32_t n_seq, int32_t vocab) {
+    QE_CHECK(n_seq >= 0 && vocab > 0, QE_ERR_INVALID_ARG);
+    QE_CHECK(vocab <= 1 << 22, QE_ERR_UNSUPPORTED);
+    QE_CHECK((int64_t)n_seq * verify_chunks(vocab) <= INT32_MAX, QE_ERR_UNSUPPORTED);
+    return QE_OK;
+}
+
+size_t qe_verify_workspace_bytes(int32_t n_seq, int32_t vocab) {
+    if (validate_verify(n_seq, vocab)) return 0;
+    return align256((size_t)n_seq * verify_chunks(vocab) * 16) + (size_t)n_seq * 4;
+}
+
+int qe_verify_drafts(const float* p, int64_t p_stride, const float* draft_p, int64_t draft_stride, int32_t vocab,
+                     const int32_t* row_start, int32_t n_rows, const int32_t* token, const int32_t* parent, const float* u,
+                     int32_t n_seq, int32_t max_rows, int32_t* taken, int32_t* path, int32_t* next, void* ws,
+                     size_t ws_bytes, void* stream) {
+    int st = validate_verify(n_seq, vocab);
+    if (st) return st;
+    QE_CHECK(n_rows >= 0 && max_rows >= 0 && p_stride >= vocab && (!draft_p || draft_stride >= vocab), QE_ERR_INVALID_ARG);
+    QE_CHECK(max_rows <= kVerifyMaxRows, QE_ERR_UNSUPPORTED);
+    QE_CHECK(!draft_p || !parent, QE_ERR_UNSUPPORTED);
+    if (n_seq == 0) return QE_OK;
+    QE_CHECK(row_start && taken && next, QE_ERR_INVALID_ARG);
+    QE_CHECK(n_rows == 0 || (p && token && u && path), QE_ERR_INVALID_ARG);
+    for (const void* a : {(const void*)p, (const void*)draft_p, (const void*)row_start, (const void*)token,
+                          (const void*)parent, (const void*)u, (const void*)taken, (const void*)path, (const void*)next,
+                          (const void*)ws})
+        QE_CHECK(aligned16(a), QE_ERR_ALIGNMENT);
+    QE_CHECK(ws && ws_bytes >= qe_verify_workspace_bytes(n_seq, vocab), QE_ERR_WORKSPACE);
+    QE_TRY_HIP(launch_verify(p, p_stride, draft_p, draft_stride, vocab, row_start, n_rows, token, parent, u, n_seq,
+                             max_rows, taken, path, next, ws, S(stream)));
     return QE_OK;
 }
 
