@@ -17,16 +17,16 @@ namespace qe {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;  // at most
 constexpr int kRopeTokens = 16;  // tokens of a workgroup at most
 
 struct RopeArgs {
     const void* x[3];
     int64_t x_stride[3];
     int heads[3];
-    int T, head_dim, tokens;  // tokens of a workgroup
+    int T, head_dim, tokens, parts;  // tokens of a workgroup, workgroups of a token
     int lanes, lane_shift;    // lanes of a head: the power of two at or above head_dim / 16
-    int rot, layout, n_pos, sec0, sec1;
+    int rot, n_pos, sec0, sec1;
     double scale;
     const double* inv_freq;
     const int32_t* pos;
@@ -35,10 +35,41 @@ struct RopeArgs {
     int q_out_bf16;
     void* cache[2];
     float* cache_scale[2];
-    int i8, page_shift;
+    int page_shift;
     uint32_t slots;
     const int32_t* slot;
 };
+
+// Sine and cosine of a (|a| < 2^33): a less the nearest multiple of pi / 2, which is taken off in two parts of 53 bits
+// each with one rounding apiece (the rest of pi / 2, below 2^-108, times 2^33 does not count), then the Taylor sums of both
+// functions on [-pi / 4, pi / 4], whose first terms left out are below 2^-54 and 2^-58: float64 values good to a few of
+// their last places, of which float32 keeps 24 bits.  The math library's sincos, whose branch for huge arguments needs
+// scratch memory, took the kernel for 4093 x 64 heads from 28 us to 160.
+__device__ inline void sin_cos(double a, double* s, double* c) {
+    constexpr double kHalfPiHi = 0x1.921fb54442d18p+0, kHalfPiLo = 0x1.1a62633145c07p-54;
+    const double n = __builtin_rint(a * 0x1.45f306dc9c883p-1);
+    const double r = __builtin_fma(-n, kHalfPiLo, __builtin_fma(-n, kHalfPiHi, a));
+    const double z = r * r;
+    double p = -1.0 / 1307674368000.0, q = 1.0 / 20922789888000.0;
+    p = __builtin_fma(p, z, 1.0 / 6227020800.0);
+    q = __builtin_fma(q, z, -1.0 / 87178291200.0);
+    p = __builtin_fma(p, z, -1.0 / 39916800.0);
+    q = __builtin_fma(q, z, 1.0 / 479001600.0);
+    p = __builtin_fma(p, z, 1.0 / 362880.0);
+    q = __builtin_fma(q, z, -1.0 / 3628800.0);
+    p = __builtin_fma(p, z, -1.0 / 5040.0);
+    q = __builtin_fma(q, z, 1.0 / 40320.0);
+    p = __builtin_fma(p, z, 1.0 / 120.0);
+    q = __builtin_fma(q, z, -1.0 / 720.0);
+    p = __builtin_fma(p, z, -1.0 / 6.0);
+    q = __builtin_fma(q, z, 1.0 / 24.0);
+    q = __builtin_fma(q, z, -0.5);
+    const double sr = __builtin_fma(r * z, p, r), cr = __builtin_fma(z, q, 1.0);
+    const int k = (int)(long long)n & 3;  // quarter turns
+    const double u = k & 1 ? cr : sr, w = k & 1 ? sr : cr;
+    *s = k & 2 ? -u : u;
+    *c = (k + 1) & 2 ? -w : w;
+}
 
 __device__ inline void store8_as(void* p, size_t idx, const float v[8], bool bf16) {
     if (bf16) {
@@ -62,10 +93,10 @@ struct Item {
     float a[8], b[8];
 };
 
-template <bool kBf16>
+template <bool kBf16, bool kPairs>
 __device__ inline void load_item(const RopeArgs& A, int item, int n_items, long t0, Item& I) {
     const int per_token = (A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift;
-    const int tok = item / per_token, rest = item - tok * per_token;
+    const int tok = A.tokens == 1 ? 0 : item / per_token, rest = item - tok * per_token;
     int head = rest >> A.lane_shift;
     const int lane = rest & (A.lanes - 1);
     I.t = t0 + tok;
@@ -86,19 +117,24 @@ __device__ inline void load_item(const RopeArgs& A, int item, int n_items, long 
     I.head = head;
     I.turn = part < 2 && lane * 16 < A.rot;
     I.pair0 = 8 * lane;
-    const bool halves = I.turn && A.layout == QE_ROPE_HALF;
+    const bool halves = I.turn && !kPairs;
     I.ch0 = halves ? 8 * lane : 16 * lane;
     I.ch1 = halves ? A.rot / 2 + 8 * lane : 16 * lane + 8;
-    const void* x = part == 0 ? A.x[0] : part == 1 ? A.x[1] : A.x[2];
-    const int64_t stride = part == 0 ? A.x_stride[0] : part == 1 ? A.x_stride[1] : A.x_stride[2];
+    // (values, not members, on the arms: a choice between members would put the arguments into scratch memory)
+    const void *xq = A.x[0], *xk = A.x[1], *xv = A.x[2];
+    const int64_t sq = A.x_stride[0], sk = A.x_stride[1], sv = A.x_stride[2];
+    const void* x = part == 0 ? xq : part == 1 ? xk : xv;
+    const int64_t stride = part == 0 ? sq : part == 1 ? sk : sv;
     const size_t at = (size_t)I.t * stride + (size_t)head * A.head_dim;
     load8(x, kBf16 ? QE_BF16 : QE_F32, at + I.ch0, I.a);
     load8(x, kBf16 ? QE_BF16 : QE_F32, at + I.ch1, I.b);
 }
 
+// (the layout is a template's: with both in one kernel the compiler keeps the channels in scratch memory)
+template <bool kPairs>
 __device__ inline void turn_item(const RopeArgs& A, const float2 (*cs)[kMaxHeadDim / 2], long t0, Item& I) {
     const float2* p = cs[I.t - t0] + I.pair0;
-    if (A.layout == QE_ROPE_HALF) {
+    if constexpr (!kPairs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float c = p[i].x, s = p[i].y, x1 = I.a[i], x2 = I.b[i];
@@ -119,6 +155,7 @@ __device__ inline void turn_item(const RopeArgs& A, const float2 (*cs)[kMaxHeadD
 }
 
 // (every lane of the wave calls it: the 8-bit form takes the largest value over a head's lanes)
+template <bool kI8>
 __device__ inline void store_item(const RopeArgs& A, const Item& I) {
     if (I.part == 0) {
         const size_t at = (size_t)I.t * A.q_out_stride + (size_t)I.head * A.head_dim;
@@ -126,7 +163,7 @@ __device__ inline void store_item(const RopeArgs& A, const Item& I) {
         store8_as(A.q_out, at + I.ch1, I.b, A.q_out_bf16);
     }
     float sx = 0.0f;
-    if (A.i8) {
+    if constexpr (kI8) {
         float m = fmaxf(absmax8(I.a), absmax8(I.b));
         for (int off = A.lanes >> 1; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
         sx = m / 127.0f;
@@ -134,48 +171,44 @@ __device__ inline void store_item(const RopeArgs& A, const Item& I) {
     if (I.part < 1) return;
     const uint32_t slot = (uint32_t)A.slot[I.t];
     if (slot >= A.slots) return;  // (negative: padding)
-    const int c = I.part - 1;
-    const int heads = c ? A.heads[2] : A.heads[1];
+    const bool val = I.part == 2;
+    const int heads = A.heads[1];
     const size_t row = ((((size_t)(slot >> A.page_shift) * heads + I.head) << A.page_shift)) +
                        (slot & ((1u << A.page_shift) - 1));
-    void* dst = c ? A.cache[1] : A.cache[0];
-    if (A.i8) {
+    void *ck = A.cache[0], *cv = A.cache[1];
+    float *ks = A.cache_scale[0], *vs = A.cache_scale[1];
+    void* dst = val ? cv : ck;
+    if constexpr (kI8) {
         uint8_t* o = reinterpret_cast<uint8_t*>(dst) + row * A.head_dim;
         *reinterpret_cast<v2u*>(o + I.ch0) = quant8(I.a, sx, 127.0f);
         *reinterpret_cast<v2u*>(o + I.ch1) = quant8(I.b, sx, 127.0f);
-        if (I.pair0 == 0) (c ? A.cache_scale[1] : A.cache_scale[0])[row] = sx;
+        if (I.pair0 == 0) (val ? vs : ks)[row] = sx;
     } else {
         store8_as(dst, row * A.head_dim + I.ch0, I.a, true);
         store8_as(dst, row * A.head_dim + I.ch1, I.b, true);
     }
 }
 
-template <bool kBf16>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A) {
+template <bool kBf16, bool kPairs, bool kI8>
+__global__ __launch_bounds__(kRopeThreads, 4) void rope_kernel(RopeArgs A) {
     __shared__ float2 cs[kRopeTokens][kMaxHeadDim / 2];
-    const long t0 = (long)blockIdx.x * A.tokens;
+    const long t0 = (long)(blockIdx.x / A.parts) * A.tokens;
     const int n_items = A.tokens * ((A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift);
-    const int wave0 = threadIdx.x & ~(kWave - 1);
-    Item now, next;
-    load_item<kBf16>(A, threadIdx.x, n_items, t0, now);  // (requested before the angles are worked out)
-    if (A.rot > 0) {
-        const int pairs = A.rot / 2;
-        for (int i = threadIdx.x; i < A.tokens * pairs; i += kRopeThreads) {
-            const int tok = i / pairs, p = i - tok * pairs;
-            if (t0 + tok >= A.T) break;
-            const int row = A.n_pos == 1 ? 0 : p < A.sec0 ? 0 : p < A.sec0 + A.sec1 ? 1 : 2;
-            double s, c;
-            sincos((double)A.pos[(size_t)row * A.T + t0 + tok] * A.inv_freq[p], &s, &c);
-            cs[tok][p] = make_float2((float)(c * A.scale), (float)(s * A.scale));
-        }
+    const int item = (int)(blockIdx.x % A.parts) * kRopeThreads + (int)threadIdx.x;
+    Item now;
+    load_item<kBf16, kPairs>(A, item, n_items, t0, now);  // (under way while the angles are worked out)
+    const int pairs = A.rot / 2;
+    for (int i = threadIdx.x; i < A.tokens * pairs; i += blockDim.x) {
+        const int tok = A.tokens == 1 ? 0 : i / pairs, p = i - tok * pairs;
+        if (t0 + tok >= A.T) break;
+        const int row = A.n_pos == 1 ? 0 : p < A.sec0 ? 0 : p < A.sec0 + A.sec1 ? 1 : 2;
+        double s, c;
+        sin_cos((double)A.pos[(size_t)row * A.T + t0 + tok] * A.inv_freq[p], &s, &c);
+        cs[tok][p] = make_float2((float)(c * A.scale), (float)(s * A.scale));
     }
     __syncthreads();
-    for (int base = 0; base + wave0 < n_items; base += kRopeThreads) {
-        load_item<kBf16>(A, base + kRopeThreads + (int)threadIdx.x, n_items, t0, next);
-        if (now.part >= 0 && now.turn) turn_item(A, cs, t0, now);
-        store_item(A, now);
-        now = next;
-    }
+    if (now.part >= 0 && now.turn) turn_item<kPairs>(A, cs, t0, now);
+    store_item<kI8>(A, now);
 }
 
 }  // namespace
@@ -192,10 +225,12 @@ hipError_t launch_rope(const RopeLaunch& R, hipStream_t st) {
     while (16 << A.lane_shift < R.head_dim) ++A.lane_shift;
     A.lanes = 1 << A.lane_shift;
     const long per_token = (long)(A.heads[0] + A.heads[1] + A.heads[2]) << A.lane_shift;
-    A.tokens = (int)std::max<long>(1, std::min<long>(kRopeTokens, kRopeThreads / per_token));
+    A.tokens = (int)std::max<long>(1, std::min<long>(kRopeTokens, 256 / per_token));
+    const long items = A.tokens * per_token;
+    A.parts = (int)((items + kRopeThreads - 1) / kRopeThreads);
+    const int threads = (int)std::min<long>(kRopeThreads, (items + kWave - 1) / kWave * kWave);
     if (R.rope) {
         A.rot = R.rope->rot_dim;
-        A.layout = R.rope->layout;
         A.n_pos = R.rope->n_pos;
         A.sec0 = R.rope->sections[0];
         A.sec1 = R.rope->sections[1];
@@ -211,14 +246,25 @@ hipError_t launch_rope(const RopeLaunch& R, hipStream_t st) {
         A.cache[1] = R.cache->v;
         A.cache_scale[0] = R.cache->k_scale;
         A.cache_scale[1] = R.cache->v_scale;
-        A.i8 = R.cache->dtype == QE_I8;
         while (1 << A.page_shift < R.cache->page_size) ++A.page_shift;
         A.slots = (uint32_t)R.cache->n_pages * (uint32_t)R.cache->page_size;
         A.slot = R.slot;
     }
-    const dim3 grid((unsigned)((R.T + A.tokens - 1) / A.tokens));
-    if (R.x_bf16) hipLaunchKernelGGL(rope_kernel<true>, grid, dim3(kRopeThreads), 0, st, A);
-    else hipLaunchKernelGGL(rope_kernel<false>, grid, dim3(kRopeThreads), 0, st, A);
+    const long groups = ((long)R.T + A.tokens - 1) / A.tokens * A.parts;
+    if (groups > INT32_MAX) return hipErrorInvalidValue;  // rejected by the caller
+    const dim3 grid((unsigned)groups);
+    const bool pairs = R.rope && R.rope->layout == QE_ROPE_PAIRS;
+    const bool i8 = R.cache && R.cache->dtype == QE_I8;
+#define QE_ROPE_LAUNCH(B, P)                                                                          \
+    do {                                                                                              \
+        if (i8) hipLaunchKernelGGL((rope_kernel<B, P, true>), grid, dim3(threads), 0, st, A);         \
+        else hipLaunchKernelGGL((rope_kernel<B, P, false>), grid, dim3(threads), 0, st, A);           \
+    } while (0)
+    if (R.x_bf16 && pairs) QE_ROPE_LAUNCH(true, true);
+    else if (R.x_bf16) QE_ROPE_LAUNCH(true, false);
+    else if (pairs) QE_ROPE_LAUNCH(false, true);
+    else QE_ROPE_LAUNCH(false, false);
+#undef QE_ROPE_LAUNCH
     return hipGetLastError();
 }
 

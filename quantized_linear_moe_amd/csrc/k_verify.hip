@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 16;                  // entries of a thread
 constexpr int kPiece = kThreads * kPer;   // entries of a piece
+constexpr int kMaxPieces = kVerifyMaxVocab / kPiece;
 
 struct VerifyArgs {
     const float *p, *d;
@@ -50,17 +51,31 @@ __device__ inline double residual(const float* p, const float* d, int j) {
     return d ? fmax(v - (double)d[j], 0.0) : v;
 }
 
-// Bits of the piece's tokens that were rejected at the last row (tree: every child of it)
-__device__ inline void drop_bits(const VerifyArgs& A, const SeqRows& r, int cur, int base, uint32_t* bits) {
-    for (int i = threadIdx.x; i < kPiece / 32; i += kThreads) bits[i] = 0;
+// Bits of the piece's tokens that were refused at the last row: every child of it
+__device__ inline void drop_bit(int above, int cur, int token, int base, uint32_t* bits) {
+    const int at = token - base;
+    if (above == cur && at >= 0 && at < kPiece) atomicOr(&bits[at >> 5], 1u << (at & 31));
+}
+
+// Sums over the threads up to and with this one (*all: over all of them), in a fixed order
+__device__ inline double block_scan(double mine, double* red, double* all) {
+    double v = mine;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const double o = __shfl_up(v, off, kWave);
+        if (threadIdx.x % kWave >= off) v += o;
+    }
+    if (threadIdx.x % kWave == kWave - 1) red[threadIdx.x / kWave] = v;
     __syncthreads();
-    if (!A.d)
-        for (int i = cur + 1 + threadIdx.x; i < r.n; i += kThreads) {
-            const int above = A.parent ? A.parent[r.first + i] : i - 1;
-            const int at = A.token[r.first + i] - base;
-            if (above == cur && at >= 0 && at < kPiece) atomicOr(&bits[at >> 5], 1u << (at & 31));
-        }
+    double before = 0.0, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kThreads / kWave; ++i) {
+        if (i == threadIdx.x / kWave) before = sum;
+        sum += red[i];
+    }
     __syncthreads();
+    *all = sum;
+    return before + v;
 }
 
 __device__ inline double block_sum(double v, double* red) {
@@ -80,6 +95,7 @@ __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
     __shared__ double red[kThreads / kWave];
     __shared__ int s_cur;
     const int seq = blockIdx.x / A.pieces, piece = blockIdx.x % A.pieces, tid = threadIdx.x;
+    for (int i = tid; i < kPiece / 32; i += kThreads) bits[i] = 0;
     const SeqRows r = rows_of(A, seq);
     if (r.n <= 0) {
         if (piece == 0 && tid == 0) {
@@ -102,18 +118,11 @@ __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
         }
     }
     __syncthreads();
-    if (!A.d && A.parent) {
-        bool again[kVerifyMaxRows / kThreads];
-#pragma unroll
-        for (int k = 0; k < kVerifyMaxRows / kThreads; ++k) {
-            const int i = tid + k * kThreads;
-            again[k] = false;
-            for (int j = 1; j < i && i < r.n; ++j) again[k] = again[k] || (par[j] == par[i] && tok[j] == tok[i]);
+    if (!A.d && A.parent) {  // a token that a sibling before it has: refused with it
+        for (int at = tid; at < r.n * r.n; at += kThreads) {
+            const int i = at / r.n, j = at - i * r.n;
+            if (j > 0 && j < i && par[j] == par[i] && tok[j] == tok[i]) pt[i] = -1.0f;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kVerifyMaxRows / kThreads; ++k)
-            if (again[k]) pt[tid + k * kThreads] = -1.0f;
         __syncthreads();
     }
     int steps = 0;
@@ -153,7 +162,10 @@ __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
     }
     __syncthreads();
     const int cur = s_cur, base = piece * kPiece;
-    drop_bits(A, r, cur, base, bits);
+    if (!A.d) {
+        for (int i = cur + 1 + tid; i < r.n; i += kThreads) drop_bit(par[i], cur, tok[i], base, bits);
+        __syncthreads();
+    }
     const float* p = A.p + (size_t)(r.first + cur) * A.p_stride;
     const float* d = A.d && cur + 1 < r.n ? A.d + (size_t)(r.first + cur + 1) * A.d_stride : nullptr;
     double sum = 0.0, all = 0.0;
@@ -173,91 +185,126 @@ __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
     }
 }
 
+// The pieces of a thread, at most kMaxPieces / kThreads consecutive ones: the sum of all, and, given a goal, the first
+// piece whose end lies past it (into *at and *before)
+constexpr int kPieces = kMaxPieces / kThreads;
+__device__ inline double scan_pieces(const double (&s)[kPieces], double* red, double (&before)[kPieces]) {
+    double mine = 0.0, all;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) mine += s[k];
+    double c = block_scan(mine, red, &all) - mine;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        before[k] = c;
+        c += s[k];
+    }
+    return all;
+}
+
+// The least `first` and the greatest `last` over the threads (one LDS atomic per wave: 4096 on one address took 30 us)
+__device__ inline void first_and_last(int first, int last, int* at_first, int* at_last) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        first = min(first, __shfl_xor(first, off, kWave));
+        last = max(last, __shfl_xor(last, off, kWave));
+    }
+    if (threadIdx.x % kWave == 0) {
+        atomicMin(at_first, first);
+        atomicMax(at_last, last);
+    }
+}
+
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs A) {
     __shared__ double R[kPiece + kThreads];  // a thread's 16 entries at 17 k: no two lanes of a group in one bank
-    __shared__ double head[kThreads / kWave];
+    __shared__ double red[kThreads / kWave];
     __shared__ uint32_t bits[kPiece / 32];
-    __shared__ double s_before, s_goal;
-    __shared__ int s_piece, s_found, s_positive;
+    __shared__ double s_before;
+    __shared__ int s_piece, s_some, s_found, s_positive;
     const int seq = blockIdx.x, tid = threadIdx.x;
+    // (what does not depend on the rows is requested with them: each wait is a trip to memory)
+    const double* sums = A.sums + (size_t)seq * A.pieces * 2;
+    const int per = (A.pieces + kThreads - 1) / kThreads;
+    double s[kPieces], s_p[kPieces], before[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int i = tid * per + k;
+        const bool in = k < per && i < A.pieces;
+        s[k] = in ? sums[2 * i] : 0.0;
+        s_p[k] = in ? sums[2 * i + 1] : 0.0;
+    }
+    const int cur = A.last[seq];
     const SeqRows r = rows_of(A, seq);
     if (r.n <= 0) return;
-    const int cur = A.last[seq];
-    const double* sums = A.sums + (size_t)seq * A.pieces * 2;
+    const double u = (double)A.u[r.first];
+    int my_above = -1, my_token = -1;  // of row tid
+    if (!A.d && tid < r.n) {
+        my_above = A.parent ? A.parent[r.first + tid] : tid - 1;
+        my_token = A.token[r.first + tid];
+    }
+    for (int i = tid; i < kPiece / 32; i += kThreads) bits[i] = 0;
     if (tid == 0) {
-        // nothing left to draw from (all of p's mass was rejected, up to its rounding): from p itself
-        double z = 0.0;
-        for (int i = 0; i < A.pieces; ++i) z += sums[2 * i];
-        int which = 0;
-        if (!(z > 0.0)) {
-            which = 1;
-            z = 0.0;
-            for (int i = 0; i < A.pieces; ++i) z += sums[2 * i + 1];
-        }
-        const double goal = (double)A.u[r.first] * z;
-        double before = 0.0;
-        int at = -1, some = -1;
-        double some_before = 0.0;
-        for (int i = 0; i < A.pieces && z > 0.0; ++i) {
-            const double s = sums[2 * i + which];
-            if (s > 0.0) {
-                some = i;
-                some_before = before;
-            }
-            if (before + s > goal) {
-                at = i;
-                break;
-            }
-            before += s;
-        }
-        s_piece = z > 0.0 ? 2 * (at >= 0 ? at : some) + which : -1;
-        s_before = at >= 0 ? before : some_before;
-        s_goal = goal;
+        s_piece = A.pieces;
+        s_some = -1;
         s_found = kPiece;
         s_positive = -1;
     }
-    __syncthreads();
-    if (s_piece < 0) {  // no distribution
+    double z = scan_pieces(s, red, before);
+    const bool plain = !(z > 0.0);  // nothing left to draw from (all of p was refused, up to its rounding): p itself
+    if (plain) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) s[k] = s_p[k];
+        z = scan_pieces(s, red, before);
+    }
+    if (!(z > 0.0)) {  // no distribution
         if (tid == 0) A.next[seq] = -1;
         return;
     }
-    const int base = (s_piece >> 1) * kPiece;
-    const bool plain = s_piece & 1;
-    drop_bits(A, r, cur, base, bits);
+    const double goal = u * z;
+    int past = A.pieces, some = -1;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+        if (s[k] > 0.0) {
+            some = tid * per + k;
+            if (before[k] + s[k] > goal) past = min(past, some);
+        }
+    first_and_last(past, some, &s_piece, &s_some);
+    __syncthreads();
+    const int piece = s_piece < A.pieces ? s_piece : s_some;  // (no piece reaches the goal: the last with any weight)
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+        if (k < per && tid * per + k == piece) s_before = before[k];
+    const int base = piece * kPiece;
+    if (!A.d && !plain) {
+        if (tid > cur) drop_bit(my_above, cur, my_token, base, bits);
+        for (int i = tid + kThreads; i < r.n; i += kThreads)
+            if (i > cur) drop_bit(A.parent ? A.parent[r.first + i] : i - 1, cur, A.token[r.first + i], base, bits);
+    }
+    __syncthreads();
     const float* p = A.p + (size_t)(r.first + cur) * A.p_stride;
     const float* d = A.d && !plain && cur + 1 < r.n ? A.d + (size_t)(r.first + cur + 1) * A.d_stride : nullptr;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int at = k * kThreads + tid;
         double v = 0.0;
-        if (base + at < A.vocab && (plain || !(bits[at >> 5] >> (at & 31) & 1u))) v = residual(p, d, base + at);
+        if (base + at < A.vocab && !(bits[at >> 5] >> (at & 31) & 1u)) v = residual(p, d, base + at);
         R[at + at / kPer] = v;
     }
     __syncthreads();
-    double mine = 0.0;
-    for (int k = 0; k < kPer; ++k) mine += R[tid * (kPer + 1) + k];
-    double before = mine;  // sums of the threads up to this one: within the wave, then the waves before it
+    double mine = 0.0, all;
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const double o = __shfl_up(before, off, kWave);
-        if (tid % kWave >= off) before += o;
-    }
-    if (tid % kWave == kWave - 1) head[tid / kWave] = before;
-    __syncthreads();
-    double c = s_before;
-    for (int i = 0; i < tid / kWave; ++i) c += head[i];
-    c += before - mine;
+    for (int k = 0; k < kPer; ++k) mine += R[tid * (kPer + 1) + k];
+    double c = s_before + (block_scan(mine, red, &all) - mine);
+    int found = kPiece, positive = -1;
+#pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const double v = R[tid * (kPer + 1) + k];
         c += v;
         if (v > 0.0) {
-            atomicMax(&s_positive, tid * kPer + k);
-            if (c > s_goal) {
-                atomicMin(&s_found, tid * kPer + k);
-                break;
-            }
+            positive = tid * kPer + k;
+            if (c > goal) found = min(found, positive);
         }
     }
+    first_and_last(found, positive, &s_found, &s_positive);
     __syncthreads();
     // (a piece whose entries sum to a little less here than in the other order: its last entry)
     if (tid == 0) A.next[seq] = base + (s_found < kPiece ? s_found : max(s_positive, 0));

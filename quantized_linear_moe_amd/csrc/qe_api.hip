@@ -730,6 +730,12 @@ int validate_stride(int64_t stride, int32_t n_heads, int32_t head_dim) {
     return QE_OK;
 }
 
+// workgroups of the rotation: a token's at most 1 + heads / 16
+int validate_tokens(int32_t T, int64_t heads) {
+    QE_CHECK((int64_t)T * (1 + heads / 16) <= INT32_MAX, QE_ERR_UNSUPPORTED);
+    return QE_OK;
+}
+
 inline bool real_dtype(int32_t d) { return d == QE_F32 || d == QE_BF16; }
 
 }  // namespace
@@ -770,6 +776,7 @@ int qe_rope_apply(const qe_rope* rope, const int32_t* pos, const void* x, int32_
     QE_CHECK(real_dtype(x_dtype) && real_dtype(y_dtype), QE_ERR_INVALID_ARG);
     if ((st = validate_stride(x_stride, n_heads, head_dim))) return st;
     if ((st = validate_stride(y_stride, n_heads, head_dim))) return st;
+    if ((st = validate_tokens(T, n_heads))) return st;
     if (T == 0) return QE_OK;
     QE_CHECK(pos && x && y, QE_ERR_INVALID_ARG);
     QE_CHECK(x != y || (x_dtype == y_dtype && x_stride == y_stride), QE_ERR_INVALID_ARG);
@@ -808,6 +815,7 @@ int qe_kv_append(const qe_kv_cache* cache, const void* k, const void* v, int32_t
     } else {
         QE_CHECK(!q && !q_out, QE_ERR_INVALID_ARG);
     }
+    if ((st = validate_tokens(T, (int64_t)n_heads + 2 * cache->n_kv_heads))) return st;
     if (T == 0) return QE_OK;
     QE_CHECK(k && v && slot && (!rope || pos), QE_ERR_INVALID_ARG);
     QE_CHECK(n_heads == 0 || (q && q_out), QE_ERR_INVALID_ARG);
@@ -901,7 +909,7 @@ int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, 
 
 static int validate_verify(int32_t n_seq, int32_t vocab) {
     QE_CHECK(n_seq >= 0 && vocab > 0, QE_ERR_INVALID_ARG);
-    QE_CHECK(vocab <= 1 << 22, QE_ERR_UNSUPPORTED);
+    QE_CHECK(vocab <= kVerifyMaxVocab, QE_ERR_UNSUPPORTED);
     QE_CHECK((int64_t)n_seq * verify_chunks(vocab) <= INT32_MAX, QE_ERR_UNSUPPORTED);
     return QE_OK;
 }

@@ -7,8 +7,7 @@
 namespace qe {
 
 constexpr int kMaxHeadDim = 256;
-constexpr int kAttnTile = 64;      // keys of a tile at most
-constexpr int kVerifyMaxRows = 1024;
+constexpr int kVerifyMaxRows = 1024, kVerifyMaxVocab = 1 << 22;
 
 // Heads to rotate or to store: q alone (qe_rope_apply), or keys and values to a cache with or without q
 struct RopeLaunch {
