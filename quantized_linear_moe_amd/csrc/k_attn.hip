@@ -109,19 +109,49 @@ struct Stage {
     static constexpr int kDma = kTileBytes / 1024 / (NT / kWave);  // 1 KB copies of a wave
     static constexpr int kUnits = BK * HD / 16 / NT;               // 16 codes each
     static constexpr int kRegs = I8 ? kUnits : 1;
+    // keys that one copy, or a wave's 16-byte loads of codes, cover: with pages of at least so many places, and every
+    // key of the tile there, they share a base address, and the lanes' offsets stay the same from tile to tile
+    static constexpr int kLanes = I8 ? HD / 16 : HD / 8;
+    static constexpr int kRun = kWave / kLanes;
     v4u rk[kRegs], rv[kRegs];
     float rks, rvs;
+    uint32_t ko[I8 ? 1 : kDma], vo;
+    int wave, lane;
 
-    // pid: the page of key k0 + lane % BK, -1 where there is none
-    __device__ inline void request(const AttnArgs& A, int head, int k0, int pid, int tid, uint32_t kbuf, uint32_t vbuf) {
+    __device__ inline void init(int tid) {
+        wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
+        lane = tid % kWave;
+        const int r = lane / kLanes, c = lane % kLanes;
+        if constexpr (I8) {
+            vo = lane * 16;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kDma; ++j)
+                ko[j] = r * HD * 2 + ((c ^ k_swizzle<HD>((wave * kDma + j) * kRun + r)) << 4);
+            vo = r * HD * 2 + ((c ^ v_swizzle<HD>(r)) << 4);  // (a run is a multiple of the swizzle's period)
+        }
+    }
+
+    // pid: the page of key k0 + lane % BK, -1 where there is none; whole: every key is there
+    __device__ inline void request(const AttnArgs& A, int head, int k0, int pid, bool whole, uint32_t kbuf, uint32_t vbuf) {
         const int mask = (1 << A.page_shift) - 1;
+        const bool runs = whole && mask + 1 >= kRun;
         if constexpr (!I8) {
-            constexpr int CH = HD / 8;
-            const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+            if (runs) {
+#pragma unroll
+                for (int j = 0; j < kDma; ++j) {
+                    const int piece = wave * kDma + j, row = piece * kRun;
+                    const uint32_t pg = __builtin_amdgcn_readlane(pid, row);
+                    const uint64_t at = ((((uint64_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * (HD * 2);
+                    dma16_at(A.k + at, ko[j], kbuf + piece * 1024);
+                    dma16_at(A.v + at, vo, vbuf + piece * 1024);
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < kDma; ++j) {
                 const int piece = wave * kDma + j;
-                const int row = piece * (kWave / CH) + lane / CH, c = lane % CH;
+                const int row = piece * kRun + lane / kLanes, c = lane % kLanes;
                 const int pg = __shfl(pid, row % BK, kWave);
                 const size_t at = ((((size_t)(uint32_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * (HD * 2);
                 const void* pk = A.k + at + ((c ^ k_swizzle<HD>(row)) << 4);
@@ -130,35 +160,45 @@ struct Stage {
                 dma16(pg < 0 ? (const void*)kZero16 : pv, vbuf + piece * 1024);
             }
         } else {
-            constexpr int CH = HD / 16;
+            if (runs) {
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                const int u = j * NT + tid, row = u / CH, c = u % CH;
-                const int pg = __shfl(pid, row % kWave, kWave);
-                const size_t at = ((((size_t)(uint32_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * HD + c * 16;
-                const uint8_t* pk = pg < 0 ? (const uint8_t*)kZero16 : A.k + at;
-                const uint8_t* pv = pg < 0 ? (const uint8_t*)kZero16 : A.v + at;
-                rk[j] = *reinterpret_cast<const v4u*>(pk);
-                rv[j] = *reinterpret_cast<const v4u*>(pv);
+                for (int j = 0; j < kUnits; ++j) {
+                    const int row = (j * (NT / kWave) + wave) * kRun;
+                    const uint32_t pg = __builtin_amdgcn_readlane(pid, row);
+                    const uint64_t at = ((((uint64_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * HD;
+                    rk[j] = *reinterpret_cast<const v4u*>(A.k + at + vo);
+                    rv[j] = *reinterpret_cast<const v4u*>(A.v + at + vo);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kUnits; ++j) {
+                    const int row = (j * (NT / kWave) + wave) * kRun + lane / kLanes, c = lane % kLanes;
+                    const int pg = __shfl(pid, row % BK, kWave);
+                    const size_t at =
+                        ((((size_t)(uint32_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * HD + c * 16;
+                    const uint8_t* pk = pg < 0 ? (const uint8_t*)kZero16 : A.k + at;
+                    const uint8_t* pv = pg < 0 ? (const uint8_t*)kZero16 : A.v + at;
+                    rk[j] = *reinterpret_cast<const v4u*>(pk);
+                    rv[j] = *reinterpret_cast<const v4u*>(pv);
+                }
             }
             rks = rvs = 0.0f;
-            if (tid < BK && pid >= 0) {
-                const size_t at = (((size_t)pid * A.n_kv + head) << A.page_shift) + ((k0 + tid) & mask);
+            if (wave == 0 && lane < BK && pid >= 0) {
+                const size_t at = (((size_t)pid * A.n_kv + head) << A.page_shift) + ((k0 + lane) & mask);
                 rks = A.ks[at];
                 rvs = A.vs[at];
             }
         }
     }
     // what was requested is in LDS (for this wave; a barrier orders the others)
-    __device__ inline void land(uint8_t* kbuf, uint8_t* vbuf, float* ksb, float* vsb, int tid) {
+    __device__ inline void land(uint8_t* kbuf, uint8_t* vbuf, float* ksb, float* vsb) {
         if constexpr (!I8) {
             QE_WAIT_VMCNT(0);
             asm volatile("" ::: "memory");
         } else {
-            constexpr int CH = HD / 16;
 #pragma unroll
             for (int j = 0; j < kUnits; ++j) {
-                const int u = j * NT + tid, row = u / CH, c = u % CH;
+                const int row = (j * (NT / kWave) + wave) * kRun + lane / kLanes, c = lane % kLanes;
                 v4u w[2];
                 codes_to_bf16(rk[j], w);
 #pragma unroll
@@ -169,9 +209,9 @@ struct Stage {
                 for (int e = 0; e < 2; ++e)
                     *reinterpret_cast<v4u*>(vbuf + row * HD * 2 + (((2 * c + e) ^ v_swizzle<HD>(row)) << 4)) = w[e];
             }
-            if (tid < BK) {
-                ksb[tid] = rks;
-                vsb[tid] = rvs;
+            if (wave == 0 && lane < BK) {
+                ksb[lane] = rks;
+                vsb[lane] = rvs;
             }
             asm volatile("" ::: "memory");
         }
@@ -202,17 +242,16 @@ struct Rows {
 };
 
 // One tile of NS x 32 keys into a wave's rows
-template <int HD, int NS, bool I8>
+template <int HD, int NS, bool I8, bool kMasked>
 __device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const float* ksb, const float* vsb,
-                                 float sc, bool masked, const uint32_t seen[NS], Rows<HD>& R) {
+                                 float sc, const uint32_t (&seen)[NS], Rows<HD>& R) {
     const int lane = threadIdx.x % kWave, r = lane % 32, h = lane / 32;
     v16f s[NS];
     const uint8_t* kp = kbuf + r * HD * 2;
     const int kx = (h ^ k_swizzle<HD>(r)) << 4;
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
+        s[b] = (v16f)(0.0f);
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) {
             const v8bf kf = *reinterpret_cast<const v8bf*>(kp + b * 32 * HD * 2 + (kx ^ (c << 5)));
@@ -227,7 +266,7 @@ __device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const
             }
         }
     }
-    if (masked) {
+    if constexpr (kMasked) {
 #pragma unroll
         for (int b = 0; b < NS; ++b) {
             const uint32_t w = seen[b] >> (4 * h);
@@ -247,9 +286,7 @@ __device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const
         R.m = m;
         R.l *= f;
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) R.o[d][i] *= f;
+        for (int d = 0; d < HD / 32; ++d) R.o[d] *= f;
     }
     v8bf p[NS][2];
 #pragma unroll
@@ -314,9 +351,7 @@ __device__ inline void load_rows(const AttnArgs& A, const Seq& q, int head, int 
         R.q[c] = __builtin_bit_cast(v8bf, w);
     }
 #pragma unroll
-    for (int d = 0; d < HD / 32; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) R.o[d][i] = 0.0f;
+    for (int d = 0; d < HD / 32; ++d) R.o[d] = (v16f)(0.0f);
     R.m = kLowest;
     R.l = 0.0f;
 }
@@ -357,7 +392,7 @@ __global__ __launch_bounds__(NW* kWave, NW == 4 ? 2 : 1) void attn_rows_kernel(A
     int hi = A.tree ? q.len : min(q.len, q.ctx + last / A.group + 1);
     if (A.splits > 1) hi = min(hi, lo + A.chunk);
 
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int wrow = row0 + 32 * wave, row = wrow + lane % 32;
     Rows<HD> R;
     load_rows<HD>(A, q, head, row, R);
@@ -365,43 +400,56 @@ __global__ __launch_bounds__(NW* kWave, NW == 4 ? 2 : 1) void attn_rows_kernel(A
     mask.token = min(row / A.group, q.n - 1);
     mask.bits = A.tree ? A.tree + (size_t)(q.first + mask.token) * A.tree_words : nullptr;
     mask.words = A.tree_words;
-    // keys that every row of the wave sees, and past which none sees any
-    const int all = q.ctx + (A.tree ? 0 : min(wrow / A.group, q.n - 1) + 1);
-    const int none = wrow >= rows ? 0 : A.tree ? q.len : q.ctx + min((wrow + 31) / A.group, q.n - 1) + 1;
+    const int all = wrow >= rows ? 0 : q.ctx + (A.tree ? 0 : wrow / A.group + 1);  // keys that every row of the wave sees
 
     const int32_t* pages = A.pages + (size_t)seq * A.max_pages;
     Stage<HD, BK, NT, I8> st;
+    st.init(tid);
     const uint32_t lds0 = lds_addr(smem);
     if (lo < hi) {
         int pid = page_of(A, pages, lo + lane, q.len);
         uint64_t valid = __ballot(pid >= 0);
-        st.request(A, head, lo, pid, tid, lds0, lds0 + 2 * TILE);
+        st.request(A, head, lo, pid, ~valid == 0, lds0, lds0 + 2 * TILE);
         pid = page_of(A, pages, lo + BK + lane, q.len);
-        st.land(smem, smem + 2 * TILE, scales, scales + 2 * BK, tid);
+        st.land(smem, smem + 2 * TILE, scales, scales + 2 * BK);
         __syncthreads();
-        int buf = 0;
-        for (int k0 = lo; k0 < hi; k0 += BK, buf ^= 1) {
-            const bool more = k0 + BK < hi;
-            const uint64_t valid_next = __ballot(pid >= 0);
+        int buf = 0, k0 = lo;
+        bool more;
+        uint64_t valid_next;
+        const auto begin = [&] {  // the next tile's rows are on their way while this one is computed
+            more = k0 + BK < hi;
+            valid_next = __ballot(pid >= 0);
             const int nb = buf ^ 1;
             if (more) {
-                st.request(A, head, k0 + BK, pid, tid, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
+                st.request(A, head, k0 + BK, pid, ~valid_next == 0, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
                 pid = page_of(A, pages, k0 + 2 * BK + lane, q.len);
             }
-            if (k0 < none) {
-                const bool masked = k0 + BK > all || k0 + BK > hi || ~valid != 0;
-                uint32_t seen[2] = {~0u, ~0u};
-                if (masked) {
-                    // (a piece ends at a multiple of the tile, or where the sequence or the tile's last row ends)
-                    seen[0] = (uint32_t)valid & mask.of(k0 - q.ctx);
-                    seen[1] = (uint32_t)(valid >> 32) & mask.of(k0 + 32 - q.ctx);
-                }
-                attn_tile<HD, 2, I8>(smem + buf * TILE, smem + (2 + buf) * TILE, scales + buf * BK,
-                                     scales + (2 + buf) * BK, A.sc, masked, seen, R);
-            }
-            if (more) st.land(smem + nb * TILE, smem + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK, tid);
+        };
+        const auto end = [&] {
+            const int nb = buf ^ 1;
+            if (more) st.land(smem + nb * TILE, smem + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK);
             valid = valid_next;
+            k0 += BK;
+            buf = nb;
             __syncthreads();
+        };
+        // tiles that need no mask first, in a loop of their own (where both forms meet, the compiler copies the running
+        // rows); after the first that does, the rest are masked
+        while (k0 < hi && k0 + BK <= all && ~valid == 0) {
+            begin();
+            const uint32_t seen[2] = {~0u, ~0u};
+            attn_tile<HD, 2, I8, false>(smem + buf * TILE, smem + (2 + buf) * TILE, scales + buf * BK,
+                                        scales + (2 + buf) * BK, A.sc, seen, R);
+            end();
+        }
+        while (k0 < hi) {
+            begin();
+            // (a piece ends at a multiple of the tile, or where the sequence or the tile's last row ends)
+            const uint32_t seen[2] = {(uint32_t)valid & mask.of(k0 - q.ctx),
+                                      (uint32_t)(valid >> 32) & mask.of(k0 + 32 - q.ctx)};
+            attn_tile<HD, 2, I8, true>(smem + buf * TILE, smem + (2 + buf) * TILE, scales + buf * BK,
+                                       scales + (2 + buf) * BK, A.sc, seen, R);
+            end();
         }
     }
     const float l = half_sum(R.l);
@@ -448,7 +496,7 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     if (rows == 0 || (split > 0 && lo >= q.len)) return;
     const int hi = A.splits > 1 ? min(q.len, lo + A.chunk) : q.len;
 
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int row = lane % 32;
     Rows<HD> R;
     load_rows<HD>(A, q, head, row, R);
@@ -460,32 +508,49 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
 
     const int32_t* pages = A.pages + (size_t)seq * A.max_pages;
     Stage<HD, BK, kWave, I8> st;
-    uint8_t* mine = smem + __builtin_amdgcn_readfirstlane(wave) * REGION;
+    st.init(lane);
+    uint8_t* mine = smem + wave * REGION;
     float* scales = scales_all + (I8 ? wave * 4 * BK : 0);
     const uint32_t lds0 = lds_addr(mine);
     int k0 = lo + wave * BK;
     if (k0 < hi) {
         int pid = page_of(A, pages, k0 + row, q.len);
         uint32_t valid = (uint32_t)__ballot(pid >= 0);
-        st.request(A, head, k0, pid, lane, lds0, lds0 + 2 * TILE);
+        st.request(A, head, k0, pid, ~valid == 0, lds0, lds0 + 2 * TILE);
         pid = page_of(A, pages, k0 + NW * BK + row, q.len);
-        st.land(mine, mine + 2 * TILE, scales, scales + 2 * BK, lane);
+        st.land(mine, mine + 2 * TILE, scales, scales + 2 * BK);
         int buf = 0;
-        for (; k0 < hi; k0 += NW * BK, buf ^= 1) {
-            const bool more = k0 + NW * BK < hi;
-            const uint32_t valid_next = (uint32_t)__ballot(pid >= 0);
+        bool more;
+        uint32_t valid_next;
+        const auto begin = [&] {
+            more = k0 + NW * BK < hi;
+            valid_next = (uint32_t)__ballot(pid >= 0);
             const int nb = buf ^ 1;
             if (more) {
-                st.request(A, head, k0 + NW * BK, pid, lane, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
+                st.request(A, head, k0 + NW * BK, pid, ~valid_next == 0, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
                 pid = page_of(A, pages, k0 + 2 * NW * BK + row, q.len);
             }
-            const bool masked = k0 + BK > all || ~valid != 0;
-            uint32_t seen[1] = {~0u};
-            if (masked) seen[0] = valid & mask.of(k0 - q.ctx);
-            attn_tile<HD, 1, I8>(mine + buf * TILE, mine + (2 + buf) * TILE, scales + buf * BK,
-                                 scales + (2 + buf) * BK, A.sc, masked, seen, R);
-            if (more) st.land(mine + nb * TILE, mine + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK, lane);
+        };
+        const auto end = [&] {
+            const int nb = buf ^ 1;
+            if (more) st.land(mine + nb * TILE, mine + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK);
             valid = valid_next;
+            k0 += NW * BK;
+            buf = nb;
+        };
+        while (k0 < hi && k0 + BK <= all && ~valid == 0) {
+            begin();
+            const uint32_t seen[1] = {~0u};
+            attn_tile<HD, 1, I8, false>(mine + buf * TILE, mine + (2 + buf) * TILE, scales + buf * BK,
+                                        scales + (2 + buf) * BK, A.sc, seen, R);
+            end();
+        }
+        while (k0 < hi) {
+            begin();
+            const uint32_t seen[1] = {valid & mask.of(k0 - q.ctx)};
+            attn_tile<HD, 1, I8, true>(mine + buf * TILE, mine + (2 + buf) * TILE, scales + buf * BK,
+                                       scales + (2 + buf) * BK, A.sc, seen, R);
+            end();
         }
     }
     // join: every wave's region holds its unnormalised rows

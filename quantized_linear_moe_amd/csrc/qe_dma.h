@@ -15,6 +15,11 @@ __device__ inline void dma16(const void* src, uint32_t lds_base) {
     asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds_base) : "memory");
 }
 
+// the same from a base address that the wave shares and a 32-bit offset per lane
+__device__ inline void dma16_at(const void* base, uint32_t offset, uint32_t lds_base) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "{m0}"(lds_base) : "memory");
+}
+
 // 4 bytes per lane: lane i writes LDS bytes [lds_base + 4 i, +4)
 __device__ inline void dma4(const void* src, uint32_t lds_base) {
     asm volatile("global_load_lds_dword %0, off" ::"v"(src), "{m0}"(lds_base) : "memory");
