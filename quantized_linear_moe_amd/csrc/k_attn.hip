@@ -102,121 +102,139 @@ __device__ inline void codes_to_bf16(v4u c, v4u out[2]) {
     }
 }
 
-// Tiles of BK keys brought to LDS by NT threads (whole waves)
-template <int HD, int BK, int NT, bool I8>
+// A sequence's page numbers, 64 at a time in the lanes and the next 64 on their way (-1: no such page)
+struct Pages {
+    const int32_t* p;
+    int n, n_pages, base, now, next;
+    uint64_t ok;  // of the 64 at hand
+
+    __device__ inline int at(int i) const {
+        if (i >= n) return -1;
+        const int v = p[i];
+        return (uint32_t)v < (uint32_t)n_pages ? v : -1;
+    }
+    __device__ inline void init(const AttnArgs& A, const Seq& q, int seq, int first) {
+        p = A.pages + (size_t)seq * A.max_pages;
+        n = (q.len + (1 << A.page_shift) - 1) >> A.page_shift;
+        n_pages = A.n_pages;
+        base = first;
+        const int lane = threadIdx.x % kWave;
+        now = at(first + lane);
+        next = at(first + kWave + lane);
+        ok = __ballot(now >= 0);
+    }
+    // the 64 with page i, which lies in them or behind
+    __device__ inline void seek(int i) {
+        while (i - base >= kWave) {
+            base += kWave;
+            now = next;
+            next = at(base + kWave + (int)(threadIdx.x % kWave));
+            ok = __ballot(now >= 0);
+        }
+    }
+    __device__ inline int page(int i) const { return __builtin_amdgcn_readlane(now, i - base); }
+    __device__ inline bool whole(int k0, int n_keys, int shift, int len) const {
+        const uint64_t need = (1 << shift) >= n_keys ? 1 : (1ull << (n_keys >> shift)) - 1;
+        return (ok >> ((k0 >> shift) - base) & need) == need && k0 + n_keys <= len;
+    }
+    // which of the n <= 64 keys from k0 on (the first of a page, or all in one) there are
+    __device__ inline uint64_t keys(int k0, int n_keys, int shift, int len) const {
+        const int i = (k0 >> shift) - base;
+        uint64_t m = ~0ull;
+        if ((1 << shift) >= n_keys) {
+            m = ok >> i & 1 ? ~0ull : 0;
+        } else {
+            const uint64_t run = (1ull << (1 << shift)) - 1;
+            m = 0;
+            for (int k = 0; k << shift < n_keys; ++k)
+                if (ok >> (i + k) & 1) m |= run << (k << shift);
+        }
+        const int left = len - k0;
+        if (left < 64) m &= left <= 0 ? 0 : (1ull << left) - 1;
+        return n_keys < 64 ? m & ((1ull << (n_keys & 63)) - 1) : m;
+    }
+};
+
+// Tiles of BK keys (or values: kV) brought to LDS by NT threads (whole waves), a wave's rows of a tile at a time: runs of
+// 16 keys, of one page each where pages have 16 places or more (kRuns), else every lane's own key
+template <int HD, int BK, int NT, bool I8, bool kV, bool kRuns>
 struct Stage {
-    static constexpr int kTileBytes = BK * HD * 2;
-    static constexpr int kDma = kTileBytes / 1024 / (NT / kWave);  // 1 KB copies of a wave
-    static constexpr int kUnits = BK * HD / 16 / NT;               // 16 codes each
-    static constexpr int kRegs = I8 ? kUnits : 1;
-    // keys that one copy, or a wave's 16-byte loads of codes, cover: with pages of at least so many places, and every
-    // key of the tile there, they share a base address, and the lanes' offsets stay the same from tile to tile
-    static constexpr int kLanes = I8 ? HD / 16 : HD / 8;
-    static constexpr int kRun = kWave / kLanes;
-    v4u rk[kRegs], rv[kRegs];
-    float rks, rvs;
-    uint32_t ko[I8 ? 1 : kDma], vo;
+    static constexpr int kRow = I8 ? HD : HD * 2;                      // bytes of a key in memory
+    static constexpr int kCount = BK * kRow / 1024 / (NT / kWave);     // 1 KB requests of a wave
+    static constexpr int kLanes = kRow / 16, kRun = kWave / kLanes;    // lanes of a key, keys of a request
+    static constexpr int kGroup = 16 / kRun;                           // requests of a run
+    static_assert(kCount * kRun % 16 == 0, "");
+    v4u codes[I8 ? kCount : 1];
+    float scale;
+    uint32_t off[kCount];  // of the lane's bytes from its run's address on
     int wave, lane;
+
+    __device__ static inline int swizzle(int row) { return kV ? v_swizzle<HD>(row) : k_swizzle<HD>(row); }
+    __device__ inline int row_of(int j) const { return (wave * kCount + j) * kRun + lane / kLanes; }
 
     __device__ inline void init(int tid) {
         wave = NT == kWave ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave);
         lane = tid % kWave;
-        const int r = lane / kLanes, c = lane % kLanes;
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            const int c = lane % kLanes;
+            off[j] = (j % kGroup * kRun + lane / kLanes) * kRow + ((I8 ? c : c ^ swizzle(row_of(j))) << 4);
+        }
+    }
+    // bytes from the cache's start to a run
+    __device__ static inline uint64_t run_at(const AttnArgs& A, int head, uint32_t page, int key) {
+        return ((((uint64_t)page * A.n_kv + head) << A.page_shift) + (key & ((1 << A.page_shift) - 1))) * kRow;
+    }
+    // from runs that are there; at[]: run_at of the wave's runs
+    __device__ inline void request_runs(const AttnArgs& A, const uint64_t (&at)[kCount / kGroup], uint32_t buf) {
+        const uint8_t* base = kV ? A.v : A.k;
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            if constexpr (I8) codes[j] = *reinterpret_cast<const v4u*>(base + at[j / kGroup] + off[j]);
+            else dma16_at(base + at[j / kGroup], off[j], buf + (wave * kCount + j) * 1024);
+        }
+    }
+    // pid: the page of key k0 + lane % BK, -1 where there is none (those keys' rows are zeros)
+    __device__ inline void request_keys(const AttnArgs& A, int head, int k0, int pid, uint32_t buf) {
+        const uint8_t* base = kV ? A.v : A.k;
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            const int row = row_of(j), c = lane % kLanes;
+            const int pg = __shfl(pid, row % BK, kWave);
+            const uint8_t* p = base + run_at(A, head, (uint32_t)pg, k0 + row) + ((I8 ? c : c ^ swizzle(row)) << 4);
+            if (pg < 0) p = reinterpret_cast<const uint8_t*>(kZero16);
+            if constexpr (I8) codes[j] = *reinterpret_cast<const v4u*>(p);
+            else dma16(p, buf + (wave * kCount + j) * 1024);
+        }
+    }
+    __device__ inline void request_scales(const AttnArgs& A, int head, int k0, int pid) {
+        scale = 0.0f;
+        if (I8 && wave == 0 && lane < BK && pid >= 0)
+            scale = (kV ? A.vs : A.ks)[run_at(A, head, (uint32_t)pid, k0 + lane) / kRow];
+    }
+    // 8-bit codes: what was requested goes to LDS (bf16 rows are copied there: wait for them)
+    __device__ inline void land(uint8_t* buf, float* scales) {
         if constexpr (I8) {
-            vo = lane * 16;
-        } else {
 #pragma unroll
-            for (int j = 0; j < kDma; ++j)
-                ko[j] = r * HD * 2 + ((c ^ k_swizzle<HD>((wave * kDma + j) * kRun + r)) << 4);
-            vo = r * HD * 2 + ((c ^ v_swizzle<HD>(r)) << 4);  // (a run is a multiple of the swizzle's period)
-        }
-    }
-
-    // pid: the page of key k0 + lane % BK, -1 where there is none; whole: every key is there
-    __device__ inline void request(const AttnArgs& A, int head, int k0, int pid, bool whole, uint32_t kbuf, uint32_t vbuf) {
-        const int mask = (1 << A.page_shift) - 1;
-        const bool runs = whole && mask + 1 >= kRun;
-        if constexpr (!I8) {
-            if (runs) {
-#pragma unroll
-                for (int j = 0; j < kDma; ++j) {
-                    const int piece = wave * kDma + j, row = piece * kRun;
-                    const uint32_t pg = __builtin_amdgcn_readlane(pid, row);
-                    const uint64_t at = ((((uint64_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * (HD * 2);
-                    dma16_at(A.k + at, ko[j], kbuf + piece * 1024);
-                    dma16_at(A.v + at, vo, vbuf + piece * 1024);
-                }
-                return;
-            }
-#pragma unroll
-            for (int j = 0; j < kDma; ++j) {
-                const int piece = wave * kDma + j;
-                const int row = piece * kRun + lane / kLanes, c = lane % kLanes;
-                const int pg = __shfl(pid, row % BK, kWave);
-                const size_t at = ((((size_t)(uint32_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * (HD * 2);
-                const void* pk = A.k + at + ((c ^ k_swizzle<HD>(row)) << 4);
-                const void* pv = A.v + at + ((c ^ v_swizzle<HD>(row)) << 4);
-                dma16(pg < 0 ? (const void*)kZero16 : pk, kbuf + piece * 1024);
-                dma16(pg < 0 ? (const void*)kZero16 : pv, vbuf + piece * 1024);
-            }
-        } else {
-            if (runs) {
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j) {
-                    const int row = (j * (NT / kWave) + wave) * kRun;
-                    const uint32_t pg = __builtin_amdgcn_readlane(pid, row);
-                    const uint64_t at = ((((uint64_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * HD;
-                    rk[j] = *reinterpret_cast<const v4u*>(A.k + at + vo);
-                    rv[j] = *reinterpret_cast<const v4u*>(A.v + at + vo);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j) {
-                    const int row = (j * (NT / kWave) + wave) * kRun + lane / kLanes, c = lane % kLanes;
-                    const int pg = __shfl(pid, row % BK, kWave);
-                    const size_t at =
-                        ((((size_t)(uint32_t)pg * A.n_kv + head) << A.page_shift) + ((k0 + row) & mask)) * HD + c * 16;
-                    const uint8_t* pk = pg < 0 ? (const uint8_t*)kZero16 : A.k + at;
-                    const uint8_t* pv = pg < 0 ? (const uint8_t*)kZero16 : A.v + at;
-                    rk[j] = *reinterpret_cast<const v4u*>(pk);
-                    rv[j] = *reinterpret_cast<const v4u*>(pv);
-                }
-            }
-            rks = rvs = 0.0f;
-            if (wave == 0 && lane < BK && pid >= 0) {
-                const size_t at = (((size_t)pid * A.n_kv + head) << A.page_shift) + ((k0 + lane) & mask);
-                rks = A.ks[at];
-                rvs = A.vs[at];
-            }
-        }
-    }
-    // what was requested is in LDS (for this wave; a barrier orders the others)
-    __device__ inline void land(uint8_t* kbuf, uint8_t* vbuf, float* ksb, float* vsb) {
-        if constexpr (!I8) {
-            QE_WAIT_VMCNT(0);
-            asm volatile("" ::: "memory");
-        } else {
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                const int row = (j * (NT / kWave) + wave) * kRun + lane / kLanes, c = lane % kLanes;
+            for (int j = 0; j < kCount; ++j) {
+                const int row = row_of(j), c = lane % kLanes;
                 v4u w[2];
-                codes_to_bf16(rk[j], w);
+                codes_to_bf16(codes[j], w);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<v4u*>(kbuf + row * HD * 2 + (((2 * c + e) ^ k_swizzle<HD>(row)) << 4)) = w[e];
-                codes_to_bf16(rv[j], w);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<v4u*>(vbuf + row * HD * 2 + (((2 * c + e) ^ v_swizzle<HD>(row)) << 4)) = w[e];
+                    *reinterpret_cast<v4u*>(buf + row * HD * 2 + (((2 * c + e) ^ swizzle(row)) << 4)) = w[e];
             }
-            if (wave == 0 && lane < BK) {
-                ksb[lane] = rks;
-                vsb[lane] = rvs;
-            }
-            asm volatile("" ::: "memory");
+            if (wave == 0 && lane < BK) scales[lane] = scale;
         }
     }
 };
+
+// Every copy of this wave has landed (rows of bf16), and its LDS writes are ordered before what follows
+template <bool I8>
+__device__ inline void landed() {
+    if constexpr (!I8) QE_WAIT_VMCNT(0);
+    asm volatile("" ::: "memory");
+}
 
 // What a lane's row sees of the 32 keys from k0 on, before the sequence's end is taken into account
 struct RowMask {
@@ -241,12 +259,10 @@ struct Rows {
     float m, l;
 };
 
-// One tile of NS x 32 keys into a wave's rows
-template <int HD, int NS, bool I8, bool kMasked>
-__device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const float* ksb, const float* vsb,
-                                 float sc, const uint32_t (&seen)[NS], Rows<HD>& R) {
+// S^T of NS x 32 keys
+template <int HD, int NS, bool I8>
+__device__ inline void attn_scores(const uint8_t* kbuf, const float* ksb, const Rows<HD>& R, v16f (&s)[NS]) {
     const int lane = threadIdx.x % kWave, r = lane % 32, h = lane / 32;
-    v16f s[NS];
     const uint8_t* kp = kbuf + r * HD * 2;
     const int kx = (h ^ k_swizzle<HD>(r)) << 4;
 #pragma unroll
@@ -257,29 +273,44 @@ __device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const
             const v8bf kf = *reinterpret_cast<const v8bf*>(kp + b * 32 * HD * 2 + (kx ^ (c << 5)));
             s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, R.q[c], s[b], 0, 0, 0);
         }
-        if constexpr (I8) {
+    }
+    if constexpr (I8) {
+#pragma unroll
+        for (int b = 0; b < NS; ++b)
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const v4f f = *reinterpret_cast<const v4f*>(ksb + 32 * b + 8 * a + 4 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[b][4 * a + i] *= f[i];
             }
-        }
     }
-    if constexpr (kMasked) {
+}
+
+// Keys that the lane's row does not see
+template <int NS>
+__device__ inline void attn_mask(const uint32_t (&seen)[NS], v16f (&s)[NS]) {
+    const int h = (threadIdx.x % kWave) / 32;
 #pragma unroll
-        for (int b = 0; b < NS; ++b) {
-            const uint32_t w = seen[b] >> (4 * h);
+    for (int b = 0; b < NS; ++b) {
+        const uint32_t w = seen[b] >> (4 * h);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[b][i] = (w >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : -__builtin_inff();
-        }
+        for (int i = 0; i < 16; ++i) s[b][i] = (w >> (8 * (i / 4) + i % 4)) & 1u ? s[b][i] : -__builtin_inff();
     }
+}
+
+template <int NS>
+__device__ inline float attn_max(const v16f (&s)[NS]) {
     float mx = s[0][0];
 #pragma unroll
     for (int b = 0; b < NS; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+    return mx;
+}
+
+// The running maximum moves where the scores (their greatest in this lane: mx) exceed it by far
+template <int HD>
+__device__ inline void attn_rescale(float mx, float sc, Rows<HD>& R) {
     mx = half_max(mx) * sc;
     if (__any(mx > R.m + kLazy)) {
         const float m = fmaxf(R.m, mx), f = __builtin_amdgcn_exp2f(R.m - m);
@@ -288,35 +319,42 @@ __device__ inline void attn_tile(const uint8_t* kbuf, const uint8_t* vbuf, const
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d) R.o[d] *= f;
     }
+}
+
+// Weights of the scores and their products with V
+template <int HD, int NS, bool I8>
+__device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float sc, const v16f (&s)[NS], Rows<HD>& R) {
+    const int lane = threadIdx.x % kWave, h = lane / 32;
     v8bf p[NS][2];
 #pragma unroll
     for (int b = 0; b < NS; ++b) {
+        v16f w = s[b];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], sc, -R.m));
+        for (int i = 0; i < 16; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], sc, -R.m));
         if constexpr (I8) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) R.l += s[b][i];
+            for (int i = 0; i < 16; ++i) R.l += w[i];
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const v4f f = *reinterpret_cast<const v4f*>(vsb + 32 * b + 8 * a + 4 * h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[b][4 * a + i] *= f[i];
+                for (int i = 0; i < 4; ++i) w[4 * a + i] *= f[i];
             }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            v4u w;
+            v4u u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const v2f two = {s[b][8 * e + 2 * i], s[b][8 * e + 2 * i + 1]};
+                const v2f two = {w[8 * e + 2 * i], w[8 * e + 2 * i + 1]};
                 const v2bf pk = __builtin_convertvector(two, v2bf);
                 if constexpr (!I8) {
                     const v2bf one = {(__bf16)1.0f, (__bf16)1.0f};
                     R.l = __builtin_amdgcn_fdot2_f32_bf16(pk, one, R.l, false);
                 }
-                w[i] = __builtin_bit_cast(uint32_t, pk);
+                u[i] = __builtin_bit_cast(uint32_t, pk);
             }
-            p[b][e] = __builtin_bit_cast(v8bf, w);
+            p[b][e] = __builtin_bit_cast(v8bf, u);
         }
     }
     // V^T: lane l reads 4 keys of channel l % 32 at a time, through its group of 16 lanes
@@ -356,12 +394,6 @@ __device__ inline void load_rows(const AttnArgs& A, const Seq& q, int head, int 
     R.l = 0.0f;
 }
 
-__device__ inline int page_of(const AttnArgs& A, const int32_t* pages, int key, int len) {
-    if (key >= len) return -1;
-    const int p = pages[key >> A.page_shift];
-    return (uint32_t)p < (uint32_t)A.n_pages ? p : -1;
-}
-
 // 4 channels of a finished row
 __device__ inline void store4(uint16_t* p, const float v[4], float f) {
     v2u w;
@@ -370,10 +402,87 @@ __device__ inline void store4(uint16_t* p, const float v[4], float f) {
     *reinterpret_cast<v2u*>(p) = w;
 }
 
+// A tile of keys as one wave sees it
+template <int BK, int NT, bool kRuns>
+struct Tile {
+    static constexpr int kGroups = BK / 16 / (NT / kWave);  // runs of 16 keys that the wave brings
+    uint64_t at[kGroups];  // where they are (whole tiles of runs)
+    uint64_t valid;        // keys that there are
+    int pid;               // the page of key k0 + lane % BK, -1 where there is none (set for tiles that are not whole, and
+                           // for every tile of codes)
+    bool whole;
+};
+
+// The tiles of a sequence, one after the other
+template <int HD, int BK, int NT, bool I8, bool kRuns>
+struct Tiles {
+    using T = Tile<BK, NT, kRuns>;
+    Pages pages;
+    Stage<HD, BK, NT, I8, false, kRuns> sk;
+    Stage<HD, BK, NT, I8, true, kRuns> sv;
+    int head, len, shift, ahead;  // ahead: the pages of the tile after, where every lane reads its own key's
+
+    __device__ inline void init(const AttnArgs& A, const Seq& q, int seq, int head_, int k0, int step, int tid) {
+        head = head_;
+        len = q.len;
+        shift = A.page_shift;
+        sk.init(tid);
+        sv.init(tid);
+        if constexpr (kRuns) {
+            pages.init(A, q, seq, k0 >> shift);
+        } else {
+            pages.p = A.pages + (size_t)seq * A.max_pages;
+            pages.n = len;
+            pages.n_pages = A.n_pages;
+            ahead = page_at(k0);
+        }
+    }
+    __device__ inline int page_at(int k0) const {  // of the lane's key
+        const int key = k0 + (int)(threadIdx.x % BK);
+        if (key >= len) return -1;
+        const int v = pages.p[key >> shift];
+        return (uint32_t)v < (uint32_t)pages.n_pages ? v : -1;
+    }
+    // step: from this tile to the next one asked for
+    __device__ inline void locate(const AttnArgs& A, int k0, int step, T& t) {
+        constexpr uint64_t kAll = BK == 64 ? ~0ull : (1ull << (BK & 63)) - 1;
+        if constexpr (kRuns) {
+            pages.seek(k0 >> shift);
+            t.whole = pages.whole(k0, BK, shift, len);
+            t.valid = kAll;
+            if (t.whole) {
+#pragma unroll
+                for (int g = 0; g < T::kGroups; ++g) {
+                    const int key = k0 + 16 * (sk.wave * T::kGroups + g);
+                    t.at[g] = sk.run_at(A, head, (uint32_t)pages.page(key >> shift), key);
+                }
+            } else {
+                t.valid = pages.keys(k0, BK, shift, len);
+            }
+            if (I8 || !t.whole) {
+                const int i = threadIdx.x % BK;
+                const int pg = __shfl(pages.now, ((k0 + i) >> shift) - pages.base, kWave);
+                t.pid = t.valid >> i & 1 ? pg : -1;
+            }
+        } else {
+            t.pid = ahead;
+            ahead = page_at(k0 + step);
+            t.valid = __ballot(t.pid >= 0) & kAll;
+            t.whole = t.valid == kAll;
+        }
+    }
+    template <bool kV, class S>
+    __device__ inline void request(const AttnArgs& A, S& s, int k0, const T& t, uint32_t buf) {
+        if (kRuns && t.whole) s.request_runs(A, t.at, buf);
+        else s.request_keys(A, head, k0, t.pid, buf);
+        if constexpr (I8) s.request_scales(A, head, k0, t.pid);
+    }
+};
+
 // Workgroup -> key head (fastest, so that a head's tiles meet in one L2), tile of rows (the last, longest one first),
 // sequence, piece
-template <int HD, int NW, bool I8>
-__global__ __launch_bounds__(NW* kWave, NW == 4 ? 2 : 1) void attn_rows_kernel(AttnArgs A) {
+template <int HD, int NW, bool I8, bool kRuns>
+__global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     constexpr int BK = 64, NT = NW * kWave, TILE = BK * HD * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * TILE];
     __shared__ __attribute__((aligned(16))) float scales[I8 ? 4 * BK : 4];
@@ -401,54 +510,65 @@ __global__ __launch_bounds__(NW* kWave, NW == 4 ? 2 : 1) void attn_rows_kernel(A
     mask.bits = A.tree ? A.tree + (size_t)(q.first + mask.token) * A.tree_words : nullptr;
     mask.words = A.tree_words;
     const int all = wrow >= rows ? 0 : q.ctx + (A.tree ? 0 : wrow / A.group + 1);  // keys that every row of the wave sees
+    const auto seen_at = [&](int k0, uint64_t valid, uint32_t (&seen)[2]) {
+        seen[0] = (uint32_t)valid & mask.of(k0 - q.ctx);
+        seen[1] = (uint32_t)(valid >> 32) & mask.of(k0 + 32 - q.ctx);
+    };
 
-    const int32_t* pages = A.pages + (size_t)seq * A.max_pages;
-    Stage<HD, BK, NT, I8> st;
-    st.init(tid);
-    const uint32_t lds0 = lds_addr(smem);
+    uint8_t *kbuf = smem, *vbuf = smem + 2 * TILE;
+    float *ksb = scales, *vsb = scales + 2 * BK;
+    const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
     if (lo < hi) {
-        int pid = page_of(A, pages, lo + lane, q.len);
-        uint64_t valid = __ballot(pid >= 0);
-        st.request(A, head, lo, pid, ~valid == 0, lds0, lds0 + 2 * TILE);
-        pid = page_of(A, pages, lo + BK + lane, q.len);
-        st.land(smem, smem + 2 * TILE, scales, scales + 2 * BK);
+        Tiles<HD, BK, NT, I8, kRuns> tiles;
+        tiles.init(A, q, seq, head, lo, BK, tid);
+        Tile<BK, NT, kRuns> t;
+        tiles.locate(A, lo, BK, t);
+        tiles.template request<false>(A, tiles.sk, lo, t, klds);
+        tiles.template request<true>(A, tiles.sv, lo, t, vlds);
+        landed<I8>();
+        tiles.sk.land(kbuf, ksb);
+        tiles.sv.land(vbuf, vsb);
         __syncthreads();
         int buf = 0, k0 = lo;
         bool more;
-        uint64_t valid_next;
-        const auto begin = [&] {  // the next tile's rows are on their way while this one is computed
+        Tile<BK, NT, kRuns> t2;
+        const auto begin = [&] {  // the next tile is on its way while this one is computed
             more = k0 + BK < hi;
-            valid_next = __ballot(pid >= 0);
-            const int nb = buf ^ 1;
             if (more) {
-                st.request(A, head, k0 + BK, pid, ~valid_next == 0, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
-                pid = page_of(A, pages, k0 + 2 * BK + lane, q.len);
+                tiles.locate(A, k0 + BK, BK, t2);
+                tiles.template request<false>(A, tiles.sk, k0 + BK, t2, klds + (buf ^ 1) * TILE);
+                tiles.template request<true>(A, tiles.sv, k0 + BK, t2, vlds + (buf ^ 1) * TILE);
             }
         };
         const auto end = [&] {
-            const int nb = buf ^ 1;
-            if (more) st.land(smem + nb * TILE, smem + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK);
-            valid = valid_next;
+            landed<I8>();
+            buf ^= 1;
+            if (more) {
+                tiles.sk.land(kbuf + buf * TILE, ksb + buf * BK);
+                tiles.sv.land(vbuf + buf * TILE, vsb + buf * BK);
+            }
+            t = t2;
             k0 += BK;
-            buf = nb;
             __syncthreads();
         };
-        // tiles that need no mask first, in a loop of their own (where both forms meet, the compiler copies the running
-        // rows); after the first that does, the rest are masked
-        while (k0 < hi && k0 + BK <= all && ~valid == 0) {
+        v16f s[2];
+        // tiles that need no mask first, in a loop of their own (where both forms meet, the compiler copies the
+        // running rows); after the first that does, the rest are masked
+        while (k0 < hi && k0 + BK <= all && t.whole) {
             begin();
-            const uint32_t seen[2] = {~0u, ~0u};
-            attn_tile<HD, 2, I8, false>(smem + buf * TILE, smem + (2 + buf) * TILE, scales + buf * BK,
-                                        scales + (2 + buf) * BK, A.sc, seen, R);
+            attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_rescale(attn_max<2>(s), A.sc, R);
+            attn_values<HD, 2, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
         while (k0 < hi) {
+            uint32_t seen[2];
+            seen_at(k0, t.valid, seen);
             begin();
-            // (a piece ends at a multiple of the tile, or where the sequence or the tile's last row ends)
-            const uint32_t seen[2] = {(uint32_t)valid & mask.of(k0 - q.ctx),
-                                      (uint32_t)(valid >> 32) & mask.of(k0 + 32 - q.ctx)};
-            attn_tile<HD, 2, I8, true>(smem + buf * TILE, smem + (2 + buf) * TILE, scales + buf * BK,
-                                       scales + (2 + buf) * BK, A.sc, seen, R);
+            attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_mask<2>(seen, s);
+            attn_rescale(attn_max<2>(s), A.sc, R);
+            attn_values<HD, 2, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
     }
@@ -478,10 +598,9 @@ __global__ __launch_bounds__(NW* kWave, NW == 4 ? 2 : 1) void attn_rows_kernel(A
 }
 
 // At most 32 rows: waves take tiles of 32 keys in turn
-template <int HD, bool I8>
+template <int HD, bool I8, bool kRuns>
 __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
-    constexpr int BK = 32, NW = 4, TILE = BK * HD * 2, OLD = HD + 4;
-    static_assert(32 * OLD * 4 <= 4 * TILE + 1024, "");
+    constexpr int BK = 32, NW = 4, STEP = NW * BK, TILE = BK * HD * 2, OLD = HD + 4;
     constexpr int REGION = 4 * TILE > 32 * OLD * 4 ? 4 * TILE : (32 * OLD * 4 + 1023) / 1024 * 1024;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * REGION];
     __shared__ __attribute__((aligned(16))) float scales_all[I8 ? NW * 4 * BK : 4];
@@ -506,50 +625,57 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     mask.words = A.tree_words;
     const int all = q.ctx + (A.tree ? 0 : 1);
 
-    const int32_t* pages = A.pages + (size_t)seq * A.max_pages;
-    Stage<HD, BK, kWave, I8> st;
-    st.init(lane);
     uint8_t* mine = smem + wave * REGION;
     float* scales = scales_all + (I8 ? wave * 4 * BK : 0);
-    const uint32_t lds0 = lds_addr(mine);
+    uint8_t *kbuf = mine, *vbuf = mine + 2 * TILE;
+    float *ksb = scales, *vsb = scales + 2 * BK;
+    const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
     int k0 = lo + wave * BK;
     if (k0 < hi) {
-        int pid = page_of(A, pages, k0 + row, q.len);
-        uint32_t valid = (uint32_t)__ballot(pid >= 0);
-        st.request(A, head, k0, pid, ~valid == 0, lds0, lds0 + 2 * TILE);
-        pid = page_of(A, pages, k0 + NW * BK + row, q.len);
-        st.land(mine, mine + 2 * TILE, scales, scales + 2 * BK);
+        Tiles<HD, BK, kWave, I8, kRuns> tiles;
+        tiles.init(A, q, seq, head, k0, STEP, lane);
+        Tile<BK, kWave, kRuns> t, t2;
+        tiles.locate(A, k0, STEP, t);
+        tiles.template request<false>(A, tiles.sk, k0, t, klds);
+        tiles.template request<true>(A, tiles.sv, k0, t, vlds);
+        landed<I8>();
+        tiles.sk.land(kbuf, ksb);
+        tiles.sv.land(vbuf, vsb);
         int buf = 0;
         bool more;
-        uint32_t valid_next;
         const auto begin = [&] {
-            more = k0 + NW * BK < hi;
-            valid_next = (uint32_t)__ballot(pid >= 0);
-            const int nb = buf ^ 1;
+            more = k0 + STEP < hi;
             if (more) {
-                st.request(A, head, k0 + NW * BK, pid, ~valid_next == 0, lds0 + nb * TILE, lds0 + (2 + nb) * TILE);
-                pid = page_of(A, pages, k0 + 2 * NW * BK + row, q.len);
+                tiles.locate(A, k0 + STEP, STEP, t2);
+                tiles.template request<false>(A, tiles.sk, k0 + STEP, t2, klds + (buf ^ 1) * TILE);
+                tiles.template request<true>(A, tiles.sv, k0 + STEP, t2, vlds + (buf ^ 1) * TILE);
             }
         };
         const auto end = [&] {
-            const int nb = buf ^ 1;
-            if (more) st.land(mine + nb * TILE, mine + (2 + nb) * TILE, scales + nb * BK, scales + (2 + nb) * BK);
-            valid = valid_next;
-            k0 += NW * BK;
-            buf = nb;
+            landed<I8>();
+            buf ^= 1;
+            if (more) {
+                tiles.sk.land(kbuf + buf * TILE, ksb + buf * BK);
+                tiles.sv.land(vbuf + buf * TILE, vsb + buf * BK);
+            }
+            t = t2;
+            k0 += STEP;
         };
-        while (k0 < hi && k0 + BK <= all && ~valid == 0) {
+        v16f s[1];
+        while (k0 < hi && k0 + BK <= all && t.whole) {
             begin();
-            const uint32_t seen[1] = {~0u};
-            attn_tile<HD, 1, I8, false>(mine + buf * TILE, mine + (2 + buf) * TILE, scales + buf * BK,
-                                        scales + (2 + buf) * BK, A.sc, seen, R);
+            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_rescale(attn_max<1>(s), A.sc, R);
+            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
         while (k0 < hi) {
+            const uint32_t seen[1] = {(uint32_t)t.valid & mask.of(k0 - q.ctx)};
             begin();
-            const uint32_t seen[1] = {valid & mask.of(k0 - q.ctx)};
-            attn_tile<HD, 1, I8, true>(mine + buf * TILE, mine + (2 + buf) * TILE, scales + buf * BK,
-                                       scales + (2 + buf) * BK, A.sc, seen, R);
+            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_mask<1>(seen, s);
+            attn_rescale(attn_max<1>(s), A.sc, R);
+            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
     }
@@ -635,13 +761,22 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs A) {
     for (int i = 0; i < V; ++i) p[i] = (uint16_t)mx4_bf16_bits(v[i] * f);
 }
 
-template <int HD, bool I8>
+template <int HD, bool I8, bool kRuns>
 void launch_hd(const AttnArgs& A, const AttnPlan& P, hipStream_t st) {
     const unsigned grid = (unsigned)((size_t)A.n_kv * P.row_tiles * A.n_seq * P.splits);
-    if (P.few_rows) hipLaunchKernelGGL((attn_keys_kernel<HD, I8>), dim3(grid), dim3(256), 0, st, A);
-    else hipLaunchKernelGGL((attn_rows_kernel<HD, 4, I8>), dim3(grid), dim3(256), 0, st, A);
+    if (P.few_rows) hipLaunchKernelGGL((attn_keys_kernel<HD, I8, kRuns>), dim3(grid), dim3(256), 0, st, A);
+    else hipLaunchKernelGGL((attn_rows_kernel<HD, 4, I8, kRuns>), dim3(grid), dim3(256), 0, st, A);
     if (P.splits > 1)
         hipLaunchKernelGGL(attn_join_kernel<HD>, dim3((unsigned)(((size_t)A.T * A.n_heads + 3) / 4)), dim3(256), 0, st, A);
+}
+
+template <int HD>
+void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
+    const bool runs = A.page_shift >= 4;
+    if (i8 && runs) launch_hd<HD, true, true>(A, P, st);
+    else if (i8) launch_hd<HD, true, false>(A, P, st);
+    else if (runs) launch_hd<HD, false, true>(A, P, st);
+    else launch_hd<HD, false, false>(A, P, st);
 }
 
 }  // namespace
@@ -698,13 +833,8 @@ hipError_t launch_attention(const AttnLaunch& L, const AttnPlan& P, hipStream_t 
     A.part_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(L.ws) +
                                         align256((size_t)P.splits * L.T * L.n_heads * 8));
     const bool i8 = c->dtype == QE_I8;
-    if (c->head_dim == 128) {
-        if (i8) launch_hd<128, true>(A, P, st);
-        else launch_hd<128, false>(A, P, st);
-    } else {
-        if (i8) launch_hd<64, true>(A, P, st);
-        else launch_hd<64, false>(A, P, st);
-    }
+    if (c->head_dim == 128) launch_any<128>(A, P, i8, st);
+    else launch_any<64>(A, P, i8, st);
     return hipGetLastError();
 }
 
