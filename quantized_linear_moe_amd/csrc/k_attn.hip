@@ -20,6 +20,7 @@
 // kernel, in order.  Keys past the sequence or of a page outside the cache are never read: their rows come from a zero
 // constant, so that whatever those places hold stays out of the products.
 #include <algorithm>
+#include <cmath>
 
 #include "qe_cache.h"
 #include "qe_dma.h"
@@ -725,40 +726,70 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     }
 }
 
-// The pieces of one token and query head, in order: a wave each
-template <int HD>
+// The pieces of one token and query head, by kPar groups of HD / 4 lanes that take every kPar-th piece in order, 8 pieces
+// of a group requested at once (one at a time, each a trip to memory: 18 us for 32 pieces, now 4)
+template <int HD, int kPar>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs A) {
-    const long id = (long)blockIdx.x * 4 + threadIdx.x / kWave;
-    const int lane = threadIdx.x % kWave;
-    const long token = id / A.n_heads;
-    const int hq = (int)(id - token * A.n_heads);
-    if (token >= A.T) return;
-    int a = 0, b = A.n_seq;  // the last sequence that starts at or before the token
-    while (b - a > 1) {
-        const int mid = (a + b) / 2;
-        if (A.q_start[mid] <= token) a = mid;
-        else b = mid;
-    }
-    const Seq q = seq_of(A, a);
-    if (token < q.first || token >= q.first + q.n) return;
+    constexpr int kLanes = HD / 4, kRows = 256 / (kLanes * kPar), kBatch = 8;
+    const int lane = threadIdx.x % kWave, c = lane % kLanes, part = lane / kLanes % kPar;
+    const unsigned per_seq = ((unsigned)A.max_q * A.n_heads + kRows - 1) / kRows;
+    const int seq = (int)(blockIdx.x / per_seq);
+    const int r = (int)(blockIdx.x - seq * per_seq) * kRows + threadIdx.x / (kLanes * kPar);  // row of the sequence
+    const Seq q = seq_of(A, seq);
+    if (r >= q.n * A.n_heads) return;
     const int n = min(A.splits, (q.len + A.chunk - 1) / A.chunk);
-    constexpr int V = HD / kWave;
-    float M = kLowest, L = 0.0f, v[V];
+    const size_t step = (size_t)A.T * A.n_heads, first = (size_t)q.first * A.n_heads + r;
+    float M = kLowest, L = 0.0f;
+    v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < n; s0 += kPar * kBatch) {
+        v4f x[kBatch];
+        float2 p[kBatch];
+        float m = M;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    for (int s = 0; s < n; ++s) M = fmaxf(M, A.part_ml[((size_t)s * A.T + token) * A.n_heads + hq].x);
-    for (int s = 0; s < n; ++s) {
-        const size_t at = ((size_t)s * A.T + token) * A.n_heads + hq;
-        const float2 p = A.part_ml[at];
-        const float w = __builtin_amdgcn_exp2f(p.x - M);
-        L += w * p.y;
+        for (int k = 0; k < kBatch; ++k) {
+            const int s = s0 + k * kPar + part;
+            p[k] = make_float2(kLowest, 0.0f);
+            x[k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if (s < n) {
+                p[k] = A.part_ml[s * step + first];
+                x[k] = *reinterpret_cast<const v4f*>(A.part_o + (s * step + first) * HD + 4 * c);
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += w * A.part_o[at * HD + V * lane + i];
+        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, p[k].x);
+        const float f = __builtin_amdgcn_exp2f(M - m);
+        M = m;
+        L *= f;
+        v *= f;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = __builtin_amdgcn_exp2f(p[k].x - M);
+            L += w * p[k].y;
+            v += w * x[k];
+        }
+    }
+#pragma unroll
+    for (int off = kLanes; off < kLanes * kPar; off <<= 1) {
+        const float m = __shfl_xor(M, off, kWave), top = fmaxf(M, m);
+        const float w = __builtin_amdgcn_exp2f(M - top), w2 = __builtin_amdgcn_exp2f(m - top);
+        M = top;
+        L = w * L + w2 * __shfl_xor(L, off, kWave);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = w * v[i] + w2 * __shfl_xor(v[i], off, kWave);
     }
     const float f = L > 0.0f ? 1.0f / L : 0.0f;
-    uint16_t* p = A.out + (size_t)token * A.out_stride + (size_t)hq * HD + V * lane;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = (uint16_t)mx4_bf16_bits(v[i] * f);
+    if (part == 0) {
+        const float u[4] = {v[0], v[1], v[2], v[3]};
+        const int token = r / A.n_heads, hq = r - token * A.n_heads;
+        store4(A.out + (size_t)(q.first + token) * A.out_stride + (size_t)hq * HD + 4 * c, u, f);
+    }
+}
+
+template <int HD, int kPar>
+void launch_join(const AttnArgs& A, hipStream_t st) {
+    constexpr int kRows = 256 / (HD / 4 * kPar);
+    hipLaunchKernelGGL((attn_join_kernel<HD, kPar>), dim3(((unsigned)A.max_q * A.n_heads + kRows - 1) / kRows * A.n_seq),
+                       dim3(256), 0, st, A);
 }
 
 template <int HD, bool I8, bool kRuns>
@@ -766,8 +797,8 @@ void launch_hd(const AttnArgs& A, const AttnPlan& P, hipStream_t st) {
     const unsigned grid = (unsigned)((size_t)A.n_kv * P.row_tiles * A.n_seq * P.splits);
     if (P.few_rows) hipLaunchKernelGGL((attn_keys_kernel<HD, I8, kRuns>), dim3(grid), dim3(256), 0, st, A);
     else hipLaunchKernelGGL((attn_rows_kernel<HD, 4, I8, kRuns>), dim3(grid), dim3(256), 0, st, A);
-    if (P.splits > 1)
-        hipLaunchKernelGGL(attn_join_kernel<HD>, dim3((unsigned)(((size_t)A.T * A.n_heads + 3) / 4)), dim3(256), 0, st, A);
+    if (P.splits > 8) launch_join<HD, 64 / (HD / 4)>(A, st);
+    else if (P.splits > 1) launch_join<HD, 1>(A, st);
 }
 
 template <int HD>
@@ -781,16 +812,26 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 
 }  // namespace
 
+// How many pieces: no more than fill the workgroups that run at once (few rows: one per CU, by its LDS; many rows: two, and
+// some more, as sequences differ), of 128 keys or more, and for many rows no more than pay: a piece's rows are written and
+// read back as float32 (8 bytes a channel at the copy rate), and 64 keys take a workgroup 1.1 us, so that pieces
+// cost `join` each and leave tiles * 1.1 / pieces to wait for, least at the root of their quotient (8 trees of 48
+// tokens, 28 heads, 4000 keys: 52 us with 6 pieces, 54 with 4, 60 with 10; one tree: 18 us with 16, 21 with 8).
+// A sequence much longer than the others is still shared by 256 workgroups, or in pieces of 8192 keys.
 AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int n_seq, int max_q, int max_kv) {
     AttnPlan P;
     const long rows = (long)max_q * (n_heads / cache->n_kv_heads);
     P.few_rows = rows <= 32;
     P.row_tiles = P.few_rows ? 1 : (int)((rows + 127) / 128);
     const long base = (long)n_seq * cache->n_kv_heads * P.row_tiles;
-    const long want = 1024, least = 256;
-    const long pieces = std::max(1L, std::min((want + base - 1) / base, (max_kv + least - 1) / least));
-    P.chunk = (int)(((max_kv + pieces - 1) / pieces + 127) / 128 * 128);
-    P.chunk = std::max(P.chunk, 128);
+    long pieces = std::min((P.few_rows ? 256 : 640) / base, (max_kv + 127) / 128L);
+    if (!P.few_rows) {
+        const double join = (double)n_seq * max_q * n_heads * cache->head_dim * 8 / 5e6;  // us
+        pieces = std::min(pieces, std::lround(std::sqrt(max_kv / 64 * 1.1 / join)));
+    }
+    const long alone = (long)cache->n_kv_heads * P.row_tiles;  // workgroups of one sequence
+    pieces = std::max({pieces, std::min((max_kv + 8191) / 8192L, (255 + alone) / alone), 1L});
+    P.chunk = (int)std::max(((max_kv + pieces - 1) / pieces + 127) / 128 * 128, 128L);
     P.splits = std::max(1, (int)(((long)max_kv + P.chunk - 1) / P.chunk));
     return P;
 }
