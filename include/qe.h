@@ -465,7 +465,7 @@ typedef struct qe_rope {
     int32_t layout;
     int32_t n_pos;
     int32_t sections[3];
-    float scale;
+    double scale;
     const double* inv_freq;
 } qe_rope;
 
@@ -482,7 +482,7 @@ typedef struct qe_kv_cache {
 } qe_kv_cache;
 
 int qe_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained_len, double slow,
-                  double fast, double* inv_freq_host, float* scale_host);
+                  double fast, double* inv_freq_host, double* scale_host);
 int qe_rope_apply(const qe_rope* rope, const int32_t* pos, const void* x, int32_t x_dtype, int64_t x_stride, int32_t T,
                   int32_t n_heads, int32_t head_dim, void* y, int32_t y_dtype, int64_t y_stride, void* stream);
 int qe_kv_append(const qe_kv_cache* cache, const void* k, const void* v, int32_t x_dtype, int64_t k_stride,

@@ -52,7 +52,7 @@ class qe_rope(ctypes.Structure):
         ("layout", ctypes.c_int32),
         ("n_pos", ctypes.c_int32),
         ("sections", ctypes.c_int32 * 3),
-        ("scale", ctypes.c_float),
+        ("scale", ctypes.c_double),
         ("inv_freq", ctypes.c_void_p),
     ]
 
@@ -358,7 +358,7 @@ def _call_on(index, where, fn, *args, stream=None):
         raise ValueError(f"{where}: needs device tensors")
     # the raw handle: making a torch.cuda.Stream for it takes as long as a small launch
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():  # (device tensors exist: CUDA is initialised)
         st = fn(*args, s)
     else:
         with torch.cuda.device(index):
@@ -468,25 +468,31 @@ def make_cache(k, v, k_scale=None, v_scale=None) -> qe_kv_cache:
 
 def _rows(where, name, t, shape, index):
     """Address and token stride of heads [T, heads, head_dim] on device `index` (dense but for the tokens)."""
+    if t.shape == shape and t.get_device() == index:
+        T, h, d = shape
+        if t.is_contiguous():
+            return t.data_ptr(), h * d
+        st = t.stride()
+        if (d == 1 or st[2] == 1) and (h == 1 or st[1] == d):
+            return t.data_ptr(), st[0] if T > 1 else h * d
+        raise ValueError(f"{where}: {name} must be dense within a token")
     if t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{where}: {name} is on {t.device}, not on device {index}")
-    T, h, d = shape
-    st = t.stride()
-    if d > 1 and st[2] != 1 or h > 1 and st[1] != d:
-        raise ValueError(f"{where}: {name} must be dense within a token")
-    return t.data_ptr(), st[0] if T > 1 else h * d
+    raise ValueError(f"{where}: {name} is on {t.device}, not on device {index}")
 
 
 def _pos(where, rope, pos, T, index):
-    return _arg(where, "pos", pos, (T,) if rope.n_pos == 1 and pos is not None and pos.dim() == 1 else (rope.n_pos, T),
-                torch.int32, index)
+    """The address of positions int32 [n_pos, T], or [T] for one row."""
+    rows = rope.n_pos
+    if pos is not None and pos.dtype is torch.int32 and pos.numel() == rows * T and pos.get_device() == index:
+        if (pos.dim() == 2 and pos.shape[0] == rows or pos.dim() == 1 and rows == 1) and pos.is_contiguous():
+            return pos.data_ptr()
+    return _arg(where, "pos", pos, (rows, T), torch.int32, index)
 
 
 def qe_rope_freqs(rot_dim, base, scaling=QE_ROPE_PLAIN, factor=1.0, trained_len=0.0, slow=1.0, fast=32.0):
     """Host inverse frequencies (float64 ndarray [rot_dim / 2]) and the factor of cosines and sines."""
-    f, s = np.empty(max(rot_dim, 0) // 2, np.float64), ctypes.c_float()
+    f, s = np.empty(max(rot_dim, 0) // 2, np.float64), ctypes.c_double()
     _check(_lib.qe_rope_freqs(rot_dim, base, scaling, factor, trained_len, slow, fast, _ptr(f), ctypes.byref(s)),
            "qe_rope_freqs")
     return f, s.value

@@ -234,7 +234,7 @@ hipError_t launch_rope(const RopeLaunch& R, hipStream_t st) {
         A.n_pos = R.rope->n_pos;
         A.sec0 = R.rope->sections[0];
         A.sec1 = R.rope->sections[1];
-        A.scale = (double)R.rope->scale;
+        A.scale = R.rope->scale;
         A.inv_freq = R.rope->inv_freq;
     }
     A.pos = R.pos;

@@ -695,7 +695,7 @@ int validate_rope(const qe_rope* r, int32_t head_dim) {
         for (int s : r->sections) QE_CHECK(s >= 0 && s <= r->rot_dim, QE_ERR_INVALID_ARG);
         QE_CHECK(2 * (r->sections[0] + r->sections[1] + r->sections[2]) == r->rot_dim, QE_ERR_INVALID_ARG);
     }
-    QE_CHECK(r->scale > 0.0f && r->scale <= 3.402823466e38f, QE_ERR_INVALID_ARG);
+    QE_CHECK(r->scale > 0.0 && std::isfinite(r->scale), QE_ERR_INVALID_ARG);
     QE_CHECK(r->rot_dim % 16 == 0, QE_ERR_UNSUPPORTED);
     QE_CHECK(r->inv_freq != nullptr, QE_ERR_INVALID_ARG);
     QE_CHECK(aligned16(r->inv_freq), QE_ERR_ALIGNMENT);
@@ -741,7 +741,7 @@ inline bool real_dtype(int32_t d) { return d == QE_F32 || d == QE_BF16; }
 }  // namespace
 
 int qe_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained_len, double slow,
-                  double fast, double* inv_freq_host, float* scale_host) {
+                  double fast, double* inv_freq_host, double* scale_host) {
     QE_CHECK(rot_dim > 0 && inv_freq_host && scale_host, QE_ERR_INVALID_ARG);
     QE_CHECK(base > 1.0 && std::isfinite(base), QE_ERR_INVALID_ARG);
     QE_CHECK(scaling >= QE_ROPE_PLAIN && scaling <= QE_ROPE_YARN, QE_ERR_INVALID_ARG);
@@ -763,7 +763,7 @@ int qe_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, 
         }
         inv_freq_host[i] = f;
     }
-    *scale_host = scaling == QE_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    *scale_host = scaling == QE_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
     return QE_OK;
 }
 

@@ -167,7 +167,7 @@ def test_frequencies(L, kind, rot, base):
     want, scale = C.freqs(rot, base, kind, 4.0, 32768, 1.0, 32.0)
     assert f.shape == (rot // 2,)
     assert np.allclose(f, want, rtol=1e-13, atol=0)
-    assert abs(s - scale) <= 2.0 ** -24 * scale
+    assert abs(s - scale) <= 1e-15 * scale
     assert np.all(np.diff(f) < 0) and f[0] <= 1.0
     if kind == "yarn":  # fast pairs keep their speed, slow ones are divided
         plain, _ = C.freqs(rot, base)
