@@ -103,25 +103,29 @@ __device__ inline void codes_to_bf16(v4u c, v4u out[2]) {
     }
 }
 
-// A sequence's page numbers, 64 at a time in the lanes and the next 64 on their way (-1: no such page)
+// A sequence's page numbers, 64 at a time in the lanes and the next 64 on their way (-1: no such page).  The first are
+// requested before the sequence's length is known, to make one trip to memory of both.
 struct Pages {
     const int32_t* p;
-    int n, n_pages, base, now, next;
+    int width, n, n_pages, base, now, next;
     uint64_t ok;  // of the 64 at hand
 
-    __device__ inline int at(int i) const {
-        if (i >= n) return -1;
-        const int v = p[i];
-        return (uint32_t)v < (uint32_t)n_pages ? v : -1;
-    }
-    __device__ inline void init(const AttnArgs& A, const Seq& q, int seq, int first) {
+    __device__ inline int read(int i) const { return (uint32_t)i < (uint32_t)width ? p[i] : -1; }
+    __device__ inline int checked(int i, int v) const { return i < n && (uint32_t)v < (uint32_t)n_pages ? v : -1; }
+    __device__ inline void early(const AttnArgs& A, int seq, int first) {
         p = A.pages + (size_t)seq * A.max_pages;
-        n = (q.len + (1 << A.page_shift) - 1) >> A.page_shift;
+        width = A.max_pages;
         n_pages = A.n_pages;
         base = first;
-        const int lane = threadIdx.x % kWave;
-        now = at(first + lane);
-        next = at(first + kWave + lane);
+        const int i = first + (int)(threadIdx.x % kWave);
+        now = read(i);
+        next = read(i + kWave);
+    }
+    __device__ inline void init(int len, int shift) {
+        n = (len + (1 << shift) - 1) >> shift;
+        const int i = base + (int)(threadIdx.x % kWave);
+        now = checked(i, now);
+        next = checked(i + kWave, next);
         ok = __ballot(now >= 0);
     }
     // the 64 with page i, which lies in them or behind
@@ -129,7 +133,8 @@ struct Pages {
         while (i - base >= kWave) {
             base += kWave;
             now = next;
-            next = at(base + kWave + (int)(threadIdx.x % kWave));
+            const int j = base + kWave + (int)(threadIdx.x % kWave);
+            next = checked(j, read(j));
             ok = __ballot(now >= 0);
         }
     }
@@ -242,7 +247,17 @@ struct RowMask {
     int token;             // of the sequence
     const uint32_t* bits;  // its tree row, or NULL
     int words;
-    __device__ inline uint32_t word(int w) const { return w < 0 ? ~0u : w >= words ? 0u : bits[w]; }
+    uint32_t w0, w1;  // the row's first words (trees of up to 64 tokens: all there are)
+    __device__ inline void init(const AttnArgs& A, const Seq& q, int row) {
+        token = min(row / A.group, q.n - 1);
+        bits = A.tree ? A.tree + (size_t)(q.first + token) * A.tree_words : nullptr;
+        words = A.tree_words;
+        w0 = A.tree ? bits[0] : 0u;
+        w1 = A.tree && words > 1 ? bits[1] : 0u;
+    }
+    __device__ inline uint32_t word(int w) const {
+        return w < 0 ? ~0u : w >= words ? 0u : w == 0 ? w0 : w == 1 ? w1 : bits[w];
+    }
     __device__ inline uint32_t of(int rel) const {  // rel: k0 less the keys before the new tokens
         if (!bits) {
             const int n = token + 1 - rel;
@@ -423,25 +438,20 @@ struct Tiles {
     Stage<HD, BK, NT, I8, true, kRuns> sv;
     int head, len, shift, ahead;  // ahead: the pages of the tile after, where every lane reads its own key's
 
-    __device__ inline void init(const AttnArgs& A, const Seq& q, int seq, int head_, int k0, int step, int tid) {
+    __device__ inline void early(const AttnArgs& A, int seq, int k0) { pages.early(A, seq, k0 >> A.page_shift); }
+    __device__ inline void init(const AttnArgs& A, const Seq& q, int head_, int k0, int tid) {
         head = head_;
         len = q.len;
         shift = A.page_shift;
         sk.init(tid);
         sv.init(tid);
-        if constexpr (kRuns) {
-            pages.init(A, q, seq, k0 >> shift);
-        } else {
-            pages.p = A.pages + (size_t)seq * A.max_pages;
-            pages.n = len;
-            pages.n_pages = A.n_pages;
-            ahead = page_at(k0);
-        }
+        if constexpr (kRuns) pages.init(len, shift);
+        else ahead = page_at(k0);
     }
     __device__ inline int page_at(int k0) const {  // of the lane's key
         const int key = k0 + (int)(threadIdx.x % BK);
         if (key >= len) return -1;
-        const int v = pages.p[key >> shift];
+        const int v = pages.read(key >> shift);
         return (uint32_t)v < (uint32_t)pages.n_pages ? v : -1;
     }
     // step: from this tile to the next one asked for
@@ -492,12 +502,13 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     id /= A.n_kv;
     const int tile = A.row_tiles - 1 - id % A.row_tiles;
     id /= A.row_tiles;
-    const int seq = id % A.n_seq, split = id / A.n_seq;
+    const int seq = id % A.n_seq, split = id / A.n_seq, lo = split * A.chunk;
+    Tiles<HD, BK, NT, I8, kRuns> tiles;
+    tiles.early(A, seq, lo);
     const Seq q = seq_of(A, seq);
     const int row0 = tile * (32 * NW), rows = q.n * A.group;
     if (row0 >= rows) return;
     const int last = min(row0 + 32 * NW, rows) - 1;
-    const int lo = split * A.chunk;
     if (split > 0 && lo >= q.len) return;  // (no such piece: the join knows the length)
     int hi = A.tree ? q.len : min(q.len, q.ctx + last / A.group + 1);
     if (A.splits > 1) hi = min(hi, lo + A.chunk);
@@ -507,9 +518,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     Rows<HD> R;
     load_rows<HD>(A, q, head, row, R);
     RowMask mask;
-    mask.token = min(row / A.group, q.n - 1);
-    mask.bits = A.tree ? A.tree + (size_t)(q.first + mask.token) * A.tree_words : nullptr;
-    mask.words = A.tree_words;
+    mask.init(A, q, row);
     const int all = wrow >= rows ? 0 : q.ctx + (A.tree ? 0 : wrow / A.group + 1);  // keys that every row of the wave sees
     const auto seen_at = [&](int k0, uint64_t valid, uint32_t (&seen)[2]) {
         seen[0] = (uint32_t)valid & mask.of(k0 - q.ctx);
@@ -520,8 +529,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     float *ksb = scales, *vsb = scales + 2 * BK;
     const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
     if (lo < hi) {
-        Tiles<HD, BK, NT, I8, kRuns> tiles;
-        tiles.init(A, q, seq, head, lo, BK, tid);
+        tiles.init(A, q, head, lo, tid);
         Tile<BK, NT, kRuns> t;
         tiles.locate(A, lo, BK, t);
         tiles.template request<false>(A, tiles.sk, lo, t, klds);
@@ -609,21 +617,21 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     int id = blockIdx.x;
     const int head = id % A.n_kv;
     id /= A.n_kv;
-    const int seq = id % A.n_seq, split = id / A.n_seq;
+    const int seq = id % A.n_seq, split = id / A.n_seq, lo = split * A.chunk;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+    int k0 = lo + wave * BK;
+    Tiles<HD, BK, kWave, I8, kRuns> tiles;
+    tiles.early(A, seq, k0);
     const Seq q = seq_of(A, seq);
     const int rows = q.n * A.group;
-    const int lo = split * A.chunk;
     if (rows == 0 || (split > 0 && lo >= q.len)) return;
     const int hi = A.splits > 1 ? min(q.len, lo + A.chunk) : q.len;
 
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
     const int row = lane % 32;
     Rows<HD> R;
     load_rows<HD>(A, q, head, row, R);
     RowMask mask;
-    mask.token = min(row / A.group, q.n - 1);
-    mask.bits = A.tree ? A.tree + (size_t)(q.first + mask.token) * A.tree_words : nullptr;
-    mask.words = A.tree_words;
+    mask.init(A, q, row);
     const int all = q.ctx + (A.tree ? 0 : 1);
 
     uint8_t* mine = smem + wave * REGION;
@@ -631,10 +639,8 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     uint8_t *kbuf = mine, *vbuf = mine + 2 * TILE;
     float *ksb = scales, *vsb = scales + 2 * BK;
     const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
-    int k0 = lo + wave * BK;
     if (k0 < hi) {
-        Tiles<HD, BK, kWave, I8, kRuns> tiles;
-        tiles.init(A, q, seq, head, k0, STEP, lane);
+        tiles.init(A, q, head, k0, lane);
         Tile<BK, kWave, kRuns> t, t2;
         tiles.locate(A, k0, STEP, t);
         tiles.template request<false>(A, tiles.sk, k0, t, klds);
@@ -818,15 +824,15 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 // cost `join` each and leave tiles * 1.1 / pieces to wait for, least at the root of their quotient (8 trees of 48
 // tokens, 28 heads, 4000 keys: 52 us with 6 pieces, 54 with 4, 60 with 10; one tree: 18 us with 16, 21 with 8).
 // A sequence much longer than the others is still shared by 256 workgroups, or in pieces of 8192 keys.
-AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int n_seq, int max_q, int max_kv) {
+AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int max_q, int max_kv) {
     AttnPlan P;
-    const long rows = (long)max_q * (n_heads / cache->n_kv_heads);
+    const long group = n_heads / cache->n_kv_heads, rows = max_q * group;
     P.few_rows = rows <= 32;
     P.row_tiles = P.few_rows ? 1 : (int)((rows + 127) / 128);
     const long base = (long)n_seq * cache->n_kv_heads * P.row_tiles;
     long pieces = std::min((P.few_rows ? 256 : 640) / base, (max_kv + 127) / 128L);
     if (!P.few_rows) {
-        const double join = (double)n_seq * max_q * n_heads * cache->head_dim * 8 / 5e6;  // us
+        const double join = std::min((double)n_seq * max_q, (double)T) * n_heads * cache->head_dim * 8 / 5e6;  // us
         pieces = std::min(pieces, std::lround(std::sqrt(max_kv / 64 * 1.1 / join)));
     }
     const long alone = (long)cache->n_kv_heads * P.row_tiles;  // workgroups of one sequence

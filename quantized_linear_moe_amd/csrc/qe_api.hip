@@ -861,7 +861,7 @@ static int validate_attention(const qe_kv_cache* cache, int32_t n_heads, int32_t
 size_t qe_attention_workspace_bytes(const qe_kv_cache* cache, int32_t n_heads, int32_t T, int32_t n_seq, int32_t max_q,
                                     int32_t max_kv) {
     if (validate_attention(cache, n_heads, T, n_seq, max_q, max_kv) || T == 0 || n_seq == 0 || max_q == 0) return 0;
-    return attn_partial_bytes(attn_plan(cache, n_heads, n_seq, max_q, max_kv), cache->head_dim, T, n_heads);
+    return attn_partial_bytes(attn_plan(cache, n_heads, T, n_seq, max_q, max_kv), cache->head_dim, T, n_heads);
 }
 
 int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, int32_t T, int32_t n_heads,
@@ -880,7 +880,7 @@ int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, 
     for (const void* p : {(const void*)q, (const void*)out, (const void*)q_start, (const void*)kv_len, (const void*)pages,
                           (const void*)tree, (const void*)ws})
         QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
-    const AttnPlan P = attn_plan(cache, n_heads, n_seq, max_q, max_kv);
+    const AttnPlan P = attn_plan(cache, n_heads, T, n_seq, max_q, max_kv);
     QE_CHECK((int64_t)cache->n_kv_heads * P.row_tiles * n_seq <= INT32_MAX / P.splits, QE_ERR_UNSUPPORTED);
     const size_t need = attn_partial_bytes(P, cache->head_dim, T, n_heads);
     QE_CHECK(ws_bytes >= need && (need == 0 || ws), QE_ERR_WORKSPACE);

@@ -32,7 +32,7 @@ struct AttnPlan {
     int splits;      // pieces of the keys (1: no partials)
     int chunk;       // keys of a piece
 };
-AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int n_seq, int max_q, int max_kv);
+AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int max_q, int max_kv);
 size_t attn_partial_bytes(const AttnPlan& P, int head_dim, int T, int n_heads);
 
 struct AttnLaunch {
