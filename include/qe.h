@@ -375,7 +375,8 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
 
 /* ------------------------------------- rotary positions, paged cache, attention --
  * What a decoder layer does between its q/k/v linears and its o linear, for prompts, for single tokens and for trees
- * of drafted tokens, and the choice among the drafts after the last layer.
+ * of drafted tokens, and the choice among the drafts after the last layer.  Arrays of positions, places, lengths, pages,
+ * tree bits, rows, tokens, probabilities and random numbers are read by the element: 4-byte alignment is enough there.
  *
  * Rotary positions (Su et al., "RoFormer"): the first rot_dim channels of a head are rot_dim / 2 pairs, and pair i of a
  * token at position pos turns by the angle pos * inv_freq[i]:
@@ -433,8 +434,9 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
  *   Products on the matrix cores with float32 sums, maxima and sums of the softmax in float32, its weights rounded to
  *   bf16 (QE_I8: after their values' scales) for the second product.  Deterministic.
  *   head_dim 64 or 128 (else QE_ERR_UNSUPPORTED), n_heads a multiple of n_kv_heads, max_kv at most 2^30, scale > 0.
- *   ws: device, qe_attention_workspace_bytes bytes (0 for many calls; 0 too for refused arguments), not shared by calls
- *   that overlap.
+ *   ws: device, qe_attention_workspace_bytes bytes of the call's own arguments (0 for many calls, and for refused
+ *   arguments; a smaller call may need more: one workspace for several calls has the largest of their sizes), not shared
+ *   by calls that overlap.
  *
  * qe_verify_drafts: how many drafted tokens of every sequence stand, and the token after them.  Sequence s has the rows
  *   row_start[s] .. row_start[s + 1] - 1: row 0 the last accepted token, every other a drafted token.  p: device float32

@@ -443,7 +443,7 @@ def make_rope(inv_freq, pairs=False, sections=None, scale=1.0) -> qe_rope:
         raise ValueError("make_rope: sections are three")
     r = qe_rope(2 * inv_freq.shape[0], QE_ROPE_PAIRS if pairs else QE_ROPE_HALF, 1 if sections is None else 3,
                 (ctypes.c_int32 * 3)(*s), scale, inv_freq.data_ptr())
-    r.tensor = inv_freq
+    r.tensor, r.device_index = inv_freq, inv_freq.get_device()
     return r
 
 
@@ -482,8 +482,10 @@ def _rows(where, name, t, shape, index):
 
 
 def _pos(where, rope, pos, T, index):
-    """The address of positions int32 [n_pos, T], or [T] for one row."""
+    """The address of positions int32 [n_pos, T], or [T] for one row (and the frequencies are on their device)."""
     rows = rope.n_pos
+    if getattr(rope, "device_index", index) != index:
+        raise ValueError(f"{where}: inv_freq is on {rope.tensor.device}, not on device {index}")
     if pos is not None and pos.dtype is torch.int32 and pos.numel() == rows * T and pos.get_device() == index:
         if (pos.dim() == 2 and pos.shape[0] == rows or pos.dim() == 1 and rows == 1) and pos.is_contiguous():
             return pos.data_ptr()

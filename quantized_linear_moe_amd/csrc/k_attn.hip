@@ -606,13 +606,15 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     }
 }
 
-// At most 32 rows: waves take tiles of 32 keys in turn
+// At most 32 rows: waves take tiles of 32 keys in turn.  Rows of bf16 are copied to the other of two buffers while a tile
+// is computed; codes wait in registers, so that one buffer does, and two workgroups fit a CU (64 sequences, 64 heads, 8192
+// keys: 135 us, with two buffers 205)
 template <int HD, bool I8, bool kRuns>
-__global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
-    constexpr int BK = 32, NW = 4, STEP = NW * BK, TILE = BK * HD * 2, OLD = HD + 4;
-    constexpr int REGION = 4 * TILE > 32 * OLD * 4 ? 4 * TILE : (32 * OLD * 4 + 1023) / 1024 * 1024;
+__global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(AttnArgs A) {
+    constexpr int BK = 32, NW = 4, STEP = NW * BK, TILE = BK * HD * 2, OLD = HD + 4, BUFS = I8 ? 1 : 2;
+    constexpr int REGION = 2 * BUFS * TILE > 32 * OLD * 4 ? 2 * BUFS * TILE : (32 * OLD * 4 + 1023) / 1024 * 1024;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NW * REGION];
-    __shared__ __attribute__((aligned(16))) float scales_all[I8 ? NW * 4 * BK : 4];
+    __shared__ __attribute__((aligned(16))) float scales_all[I8 ? NW * 2 * BK : 4];
     __shared__ float2 ml[NW][32];
     int id = blockIdx.x;
     const int head = id % A.n_kv;
@@ -635,9 +637,9 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
     const int all = q.ctx + (A.tree ? 0 : 1);
 
     uint8_t* mine = smem + wave * REGION;
-    float* scales = scales_all + (I8 ? wave * 4 * BK : 0);
-    uint8_t *kbuf = mine, *vbuf = mine + 2 * TILE;
-    float *ksb = scales, *vsb = scales + 2 * BK;
+    float* scales = scales_all + (I8 ? wave * 2 * BK : 0);
+    uint8_t *kbuf = mine, *vbuf = mine + BUFS * TILE;
+    float *ksb = scales, *vsb = scales + BK;
     const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
     if (k0 < hi) {
         tiles.init(A, q, head, k0, lane);
@@ -660,10 +662,10 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
         };
         const auto end = [&] {
             landed<I8>();
-            buf ^= 1;
+            if (!I8) buf ^= 1;
             if (more) {
-                tiles.sk.land(kbuf + buf * TILE, ksb + buf * BK);
-                tiles.sv.land(vbuf + buf * TILE, vsb + buf * BK);
+                tiles.sk.land(kbuf, ksb);
+                tiles.sv.land(vbuf, vsb);
             }
             t = t2;
             k0 += STEP;
@@ -671,18 +673,18 @@ __global__ __launch_bounds__(256) void attn_keys_kernel(AttnArgs A) {
         v16f s[1];
         while (k0 < hi && k0 + BK <= all && t.whole) {
             begin();
-            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
+            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb, A.sc, s, R);
             end();
         }
         while (k0 < hi) {
             const uint32_t seen[1] = {(uint32_t)t.valid & mask.of(k0 - q.ctx)};
             begin();
-            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
+            attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_mask<1>(seen, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
+            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb, A.sc, s, R);
             end();
         }
     }
@@ -818,19 +820,27 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 
 }  // namespace
 
-// How many pieces: no more than fill the workgroups that run at once (few rows: one per CU, by its LDS; many rows: two, and
-// some more, as sequences differ), of 128 keys or more, and for many rows no more than pay: a piece's rows are written and
-// read back as float32 (8 bytes a channel at the copy rate), and 64 keys take a workgroup 1.1 us, so that pieces
-// cost `join` each and leave tiles * 1.1 / pieces to wait for, least at the root of their quotient (8 trees of 48
-// tokens, 28 heads, 4000 keys: 52 us with 6 pieces, 54 with 4, 60 with 10; one tree: 18 us with 16, 21 with 8).
-// A sequence much longer than the others is still shared by 256 workgroups, or in pieces of 8192 keys.
+// How many pieces: as many as fill the workgroups that run at once (few rows: 1 to 3 per CU, by LDS and registers; many
+// rows: two, and some more, as sequences differ), of 128 keys or more.
+//   Few rows, as many sequences and heads as run at once already: pieces for two rounds (where several workgroups share a
+//   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads, 8-bit
+//   cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
+//   Many rows: no more than pay.  A piece's rows are written and read back as float32 (8 bytes a channel at the copy
+//   rate), and 64 keys take a workgroup 1.1 us, so that pieces cost `join` each and leave tiles * 1.1 / pieces to wait for,
+//   least at the root of their quotient (8 trees of 48 tokens, 28 heads, 4000 keys: 52 us with 6 pieces, 54 with 4,
+//   60 with 10; one tree: 18 us with 16, 21 with 8).  A sequence much longer than the others is still shared by 256
+//   workgroups, or in pieces of 8192 keys.
 AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int max_q, int max_kv) {
     AttnPlan P;
     const long group = n_heads / cache->n_kv_heads, rows = max_q * group;
     P.few_rows = rows <= 32;
     P.row_tiles = P.few_rows ? 1 : (int)((rows + 127) / 128);
     const long base = (long)n_seq * cache->n_kv_heads * P.row_tiles;
-    long pieces = std::min((P.few_rows ? 256 : 640) / base, (max_kv + 127) / 128L);
+    const bool i8 = cache->dtype == QE_I8, narrow = cache->head_dim == 64;
+    const long at_once = !P.few_rows ? 640 : i8 ? (narrow ? 768 : 512) : narrow ? 512 : 256;
+    long pieces = std::min(at_once / base, (max_kv + 127) / 128L);
+    if (P.few_rows && at_once < 2 * base)
+        pieces = std::min(((at_once > 256 ? 4 : 2) * at_once + base - 1) / base, max_kv / 512L);
     if (!P.few_rows) {
         const double join = std::min((double)n_seq * max_q, (double)T) * n_heads * cache->head_dim * 8 / 5e6;  // us
         pieces = std::min(pieces, std::lround(std::sqrt(max_kv / 64 * 1.1 / join)));

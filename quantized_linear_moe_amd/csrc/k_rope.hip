@@ -251,7 +251,6 @@ hipError_t launch_rope(const RopeLaunch& R, hipStream_t st) {
         A.slot = R.slot;
     }
     const long groups = ((long)R.T + A.tokens - 1) / A.tokens * A.parts;
-    if (groups > INT32_MAX) return hipErrorInvalidValue;  // rejected by the caller
     const dim3 grid((unsigned)groups);
     const bool pairs = R.rope && R.rope->layout == QE_ROPE_PAIRS;
     const bool i8 = R.cache && R.cache->dtype == QE_I8;

@@ -57,6 +57,7 @@ inline bool mx4(const qe_linear* lin) { return lin->a_bits == 4; }
 inline bool int_codes(const qe_linear* lin) { return lin->a_bits == 6 || lin->a_bits == 8; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }  // arrays read by the element
 
 int validate_linear(const qe_linear* lin) {
     QE_CHECK(lin != nullptr, QE_ERR_INVALID_ARG);
@@ -730,9 +731,12 @@ int validate_stride(int64_t stride, int32_t n_heads, int32_t head_dim) {
     return QE_OK;
 }
 
+// A launch counts its threads in 32 bits
+constexpr int64_t kMaxGroups = ((int64_t)1 << 32) / 256 - 1;
+
 // workgroups of the rotation: a token's at most 1 + heads / 16
 int validate_tokens(int32_t T, int64_t heads) {
-    QE_CHECK((int64_t)T * (1 + heads / 16) <= INT32_MAX, QE_ERR_UNSUPPORTED);
+    QE_CHECK((int64_t)T * (1 + heads / 16) <= kMaxGroups, QE_ERR_UNSUPPORTED);
     return QE_OK;
 }
 
@@ -780,7 +784,7 @@ int qe_rope_apply(const qe_rope* rope, const int32_t* pos, const void* x, int32_
     if (T == 0) return QE_OK;
     QE_CHECK(pos && x && y, QE_ERR_INVALID_ARG);
     QE_CHECK(x != y || (x_dtype == y_dtype && x_stride == y_stride), QE_ERR_INVALID_ARG);
-    for (const void* p : {(const void*)pos, x, (const void*)y}) QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_CHECK(aligned16(x) && aligned16(y) && aligned4(pos), QE_ERR_ALIGNMENT);
     RopeLaunch R = {};
     R.x[0] = x;
     R.x_stride[0] = x_stride;
@@ -820,8 +824,8 @@ int qe_kv_append(const qe_kv_cache* cache, const void* k, const void* v, int32_t
     QE_CHECK(k && v && slot && (!rope || pos), QE_ERR_INVALID_ARG);
     QE_CHECK(n_heads == 0 || (q && q_out), QE_ERR_INVALID_ARG);
     QE_CHECK(!q || q != q_out || (x_dtype == q_out_dtype && q_stride == q_out_stride), QE_ERR_INVALID_ARG);
-    for (const void* p : {k, v, (const void*)slot, (const void*)pos, q, (const void*)q_out})
-        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    for (const void* p : {k, v, q, (const void*)q_out}) QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_CHECK(aligned4(slot) && aligned4(pos), QE_ERR_ALIGNMENT);
     RopeLaunch R = {};
     const void* x[3] = {n_heads ? q : nullptr, k, v};
     const int64_t strides[3] = {q_stride, k_stride, v_stride};
@@ -853,7 +857,7 @@ static int validate_attention(const qe_kv_cache* cache, int32_t n_heads, int32_t
     QE_CHECK(T >= 0 && n_seq >= 0 && max_q >= 0 && max_kv >= 0, QE_ERR_INVALID_ARG);
     QE_CHECK(n_heads <= 4096 && (cache->head_dim == 64 || cache->head_dim == 128), QE_ERR_UNSUPPORTED);
     QE_CHECK(max_kv <= 1 << 30, QE_ERR_UNSUPPORTED);
-    // rows of a sequence and key head, and workgroups, are counted in 31 bits
+    // a sequence's rows are counted in 31 bits
     QE_CHECK((int64_t)max_q * n_heads <= 1 << 30 && (int64_t)T * n_heads <= (int64_t)1 << 32, QE_ERR_UNSUPPORTED);
     return QE_OK;
 }
@@ -877,11 +881,12 @@ int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, 
     if (T == 0 || n_seq == 0 || max_q == 0) return QE_OK;
     QE_CHECK(q && out && q_start && kv_len && (pages || max_pages == 0), QE_ERR_INVALID_ARG);
     QE_CHECK(q != out, QE_ERR_INVALID_ARG);
-    for (const void* p : {(const void*)q, (const void*)out, (const void*)q_start, (const void*)kv_len, (const void*)pages,
-                          (const void*)tree, (const void*)ws})
-        QE_CHECK(aligned16(p), QE_ERR_ALIGNMENT);
+    QE_CHECK(aligned16(q) && aligned16(out) && aligned16(ws), QE_ERR_ALIGNMENT);
+    for (const void* p : {(const void*)q_start, (const void*)kv_len, (const void*)pages, (const void*)tree})
+        QE_CHECK(aligned4(p), QE_ERR_ALIGNMENT);
     const AttnPlan P = attn_plan(cache, n_heads, T, n_seq, max_q, max_kv);
-    QE_CHECK((int64_t)cache->n_kv_heads * P.row_tiles * n_seq <= INT32_MAX / P.splits, QE_ERR_UNSUPPORTED);
+    QE_CHECK((int64_t)cache->n_kv_heads * P.row_tiles * n_seq <= kMaxGroups / P.splits, QE_ERR_UNSUPPORTED);
+    QE_CHECK(P.splits == 1 || ((int64_t)max_q * n_heads / 4 + 1) * n_seq <= kMaxGroups, QE_ERR_UNSUPPORTED);
     const size_t need = attn_partial_bytes(P, cache->head_dim, T, n_heads);
     QE_CHECK(ws_bytes >= need && (need == 0 || ws), QE_ERR_WORKSPACE);
     AttnLaunch A = {};
@@ -910,7 +915,7 @@ int qe_attention(const qe_kv_cache* cache, const uint16_t* q, int64_t q_stride, 
 static int validate_verify(int32_t n_seq, int32_t vocab) {
     QE_CHECK(n_seq >= 0 && vocab > 0, QE_ERR_INVALID_ARG);
     QE_CHECK(vocab <= kVerifyMaxVocab, QE_ERR_UNSUPPORTED);
-    QE_CHECK((int64_t)n_seq * verify_chunks(vocab) <= INT32_MAX, QE_ERR_UNSUPPORTED);
+    QE_CHECK((int64_t)n_seq * verify_chunks(vocab) <= kMaxGroups, QE_ERR_UNSUPPORTED);
     return QE_OK;
 }
 
@@ -932,9 +937,9 @@ int qe_verify_drafts(const float* p, int64_t p_stride, const float* draft_p, int
     QE_CHECK(row_start && taken && next, QE_ERR_INVALID_ARG);
     QE_CHECK(n_rows == 0 || (p && token && u && path), QE_ERR_INVALID_ARG);
     for (const void* a : {(const void*)p, (const void*)draft_p, (const void*)row_start, (const void*)token,
-                          (const void*)parent, (const void*)u, (const void*)taken, (const void*)path, (const void*)next,
-                          (const void*)ws})
-        QE_CHECK(aligned16(a), QE_ERR_ALIGNMENT);
+                          (const void*)parent, (const void*)u, (const void*)taken, (const void*)path, (const void*)next})
+        QE_CHECK(aligned4(a), QE_ERR_ALIGNMENT);
+    QE_CHECK(aligned16(ws), QE_ERR_ALIGNMENT);
     QE_CHECK(ws && ws_bytes >= qe_verify_workspace_bytes(n_seq, vocab), QE_ERR_WORKSPACE);
     QE_TRY_HIP(launch_verify(p, p_stride, draft_p, draft_stride, vocab, row_start, n_rows, token, parent, u, n_seq,
                              max_rows, taken, path, next, ws, S(stream)));

@@ -67,9 +67,9 @@ def test_rope_refusals(L):
         ({0: None}, "INVALID_ARG"), ({1: None}, "INVALID_ARG"), ({2: None}, "INVALID_ARG"), ({8: None}, "INVALID_ARG"),
         ({3: 2}, "INVALID_ARG"), ({9: -1}, "INVALID_ARG"), ({4: 248}, "INVALID_ARG"), ({4: 260}, "ALIGNMENT"),
         ({10: 255}, "INVALID_ARG"), ({10: 257}, "ALIGNMENT"), ({5: -1}, "INVALID_ARG"), ({6: 0}, "INVALID_ARG"),
-        ({6: 4097}, "UNSUPPORTED"), ({7: 0}, "INVALID_ARG"), ({7: 72, 4: 288, 10: 288}, "UNSUPPORTED"),
+        ({5: 2 ** 31 - 1}, "UNSUPPORTED"), ({6: 4097}, "UNSUPPORTED"), ({7: 0}, "INVALID_ARG"), ({7: 72, 4: 288, 10: 288}, "UNSUPPORTED"),
         ({7: 272, 4: 2048, 10: 2048}, "UNSUPPORTED"), ({8: P, 10: 264}, "INVALID_ARG"), ({8: P, 9: 0}, "INVALID_ARG"),
-        ({1: P + 4}, "ALIGNMENT"), ({2: P + 2}, "ALIGNMENT"), ({8: 2 * P + 8}, "ALIGNMENT")])
+        ({1: P + 2}, "ALIGNMENT"), ({2: P + 4}, "ALIGNMENT"), ({8: 2 * P + 8}, "ALIGNMENT")])
     args = list(good)
     args[1] = args[2] = args[8] = None
     args[5] = 0
@@ -86,9 +86,9 @@ def test_append_refusals(L):
         ({0: None}, "INVALID_ARG"), ({1: None}, "INVALID_ARG"), ({2: None}, "INVALID_ARG"), ({7: None}, "INVALID_ARG"),
         ({9: None}, "INVALID_ARG"), ({10: None}, "INVALID_ARG"), ({13: None}, "INVALID_ARG"), ({12: 0}, "INVALID_ARG"),
         ({12: -1}, "INVALID_ARG"), ({12: 5000}, "UNSUPPORTED"), ({3: 2}, "INVALID_ARG"), ({14: 2}, "INVALID_ARG"),
-        ({4: 120}, "INVALID_ARG"), ({5: 130}, "ALIGNMENT"), ({6: -1}, "INVALID_ARG"), ({11: 248}, "INVALID_ARG"),
+        ({4: 120}, "INVALID_ARG"), ({5: 130}, "ALIGNMENT"), ({6: -1}, "INVALID_ARG"), ({6: 2 ** 30}, "UNSUPPORTED"), ({11: 248}, "INVALID_ARG"),
         ({15: 258}, "ALIGNMENT"), ({13: P, 15: 512}, "INVALID_ARG"), ({13: P, 14: 0}, "INVALID_ARG"),
-        ({1: P + 2}, "ALIGNMENT"), ({7: P + 4}, "ALIGNMENT"), ({9: P + 4}, "ALIGNMENT"), ({13: 2 * P + 2}, "ALIGNMENT")])
+        ({1: P + 4}, "ALIGNMENT"), ({7: P + 2}, "ALIGNMENT"), ({9: P + 1}, "ALIGNMENT"), ({13: 2 * P + 4}, "ALIGNMENT")])
     args = list(good)
     for i in (1, 2, 7, 9, 10, 13):
         args[i] = None
@@ -112,10 +112,10 @@ def test_attention_refusals(L):
         ({16: 0}, "INVALID_ARG"), ({3: -1}, "INVALID_ARG"), ({4: 0}, "INVALID_ARG"), ({4: 3}, "INVALID_ARG"),
         ({4: 4098, 2: 4098 * 64, 16: 4098 * 64}, "UNSUPPORTED"), ({8: -1}, "INVALID_ARG"), ({9: -1}, "INVALID_ARG"),
         ({10: -1}, "INVALID_ARG"), ({11: -1}, "INVALID_ARG"), ({11: 2 ** 30 + 1}, "UNSUPPORTED"),
-        ({10: 2 ** 29}, "UNSUPPORTED"), ({12: P, 13: 0}, "INVALID_ARG"), ({14: 0.0}, "INVALID_ARG"),
+        ({10: 2 ** 29}, "UNSUPPORTED"), ({8: 2 ** 30}, "UNSUPPORTED"), ({12: P, 13: 0}, "INVALID_ARG"), ({14: 0.0}, "INVALID_ARG"),
         ({14: -1.0}, "INVALID_ARG"), ({14: float("nan")}, "INVALID_ARG"), ({14: float("inf")}, "INVALID_ARG"),
         ({17: None}, "WORKSPACE"), ({18: need - 1}, "WORKSPACE"), ({17: P + 8}, "ALIGNMENT"), ({1: P + 8}, "ALIGNMENT"),
-        ({5: P + 4}, "ALIGNMENT"), ({7: P + 4}, "ALIGNMENT"), ({12: P + 4, 13: 1}, "ALIGNMENT")])
+        ({5: P + 2}, "ALIGNMENT"), ({6: P + 1}, "ALIGNMENT"), ({7: P + 2}, "ALIGNMENT"), ({12: P + 2, 13: 1}, "ALIGNMENT")])
     for at in (3, 8, 10):  # no tokens, no sequences
         args = list(good)
         args[at] = 0
@@ -147,10 +147,10 @@ def test_verify_refusals(L):
     _refused(L, f, good, [
         ({0: None}, "INVALID_ARG"), ({1: 999}, "INVALID_ARG"), ({3: 999}, "INVALID_ARG"), ({4: 0}, "INVALID_ARG"),
         ({4: 2 ** 22 + 1, 1: 2 ** 23, 3: 2 ** 23}, "UNSUPPORTED"), ({5: None}, "INVALID_ARG"), ({6: -1}, "INVALID_ARG"),
-        ({7: None}, "INVALID_ARG"), ({8: P}, "UNSUPPORTED"), ({9: None}, "INVALID_ARG"), ({10: -1}, "INVALID_ARG"),
+        ({7: None}, "INVALID_ARG"), ({8: P}, "UNSUPPORTED"), ({9: None}, "INVALID_ARG"), ({10: -1}, "INVALID_ARG"), ({10: 2 ** 30}, "UNSUPPORTED"),
         ({11: -1}, "INVALID_ARG"), ({11: 1025}, "UNSUPPORTED"), ({12: None}, "INVALID_ARG"), ({13: None}, "INVALID_ARG"),
-        ({14: None}, "INVALID_ARG"), ({15: None}, "WORKSPACE"), ({16: need - 1}, "WORKSPACE"), ({0: P + 4}, "ALIGNMENT"),
-        ({2: P + 4}, "ALIGNMENT"), ({7: P + 4}, "ALIGNMENT"), ({15: P + 8}, "ALIGNMENT")])
+        ({14: None}, "INVALID_ARG"), ({15: None}, "WORKSPACE"), ({16: need - 1}, "WORKSPACE"), ({0: P + 2}, "ALIGNMENT"),
+        ({2: P + 2}, "ALIGNMENT"), ({7: P + 1}, "ALIGNMENT"), ({15: P + 8}, "ALIGNMENT")])
     args = list(good)
     args[10] = 0
     args[5] = args[12] = args[14] = args[15] = None

@@ -282,6 +282,15 @@ def test_long_contexts_in_pieces(L, n, tree, i8):
     assert torch.equal(out, b.run(L))
 
 
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("heads,kv", [(33, 1), (64, 1), (160, 2), (31, 1), (32, 1)])
+def test_wide_groups(L, heads, kv, i8):
+    """Groups of query heads around and past the 32 rows of a wave and the 128 of a tile."""
+    for lens in ([(1, 77), (1, 300)], [(3, 50), (2, 129)]):
+        b = Batch(L, lens, heads, kv, 64, 16, i8, seed=heads)
+        b.check(b.run(L))
+
+
 def test_bounds_above_the_lengths_change_nothing_visible(L):
     """A launch chosen for longer contexts and more tokens gives rows within the bound too."""
     for n in (1, 20):
