@@ -57,14 +57,29 @@ __device__ inline void drop_bit(int above, int cur, int token, int base, uint32_
     if (above == cur && at >= 0 && at < kPiece) atomicOr(&bits[at >> 5], 1u << (at & 31));
 }
 
+// A double from the lane that a data-parallel move names (0 where there is none, and in the rows left out)
+template <int kCtrl, int kRows>
+__device__ inline double moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRows, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sums over the wave's lanes up to and with this one: within rows of 16, then the rows before (lane moves: through LDS, each
+// of the six steps is a trip there, and the draw took 9.9 us in place of 9.1)
+__device__ inline double wave_scan(double v) {
+    v += moved<0x111, 0xF>(v);  // from 1, 2, 4, 8 lanes below
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);  // lane 15 of rows 0 and 2 to the row above
+    v += moved<0x143, 0xC>(v);  // lane 31 to the upper half
+    return v;
+}
+
 // Sums over the threads up to and with this one (*all: over all of them), in a fixed order
 __device__ inline double block_scan(double mine, double* red, double* all) {
-    double v = mine;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const double o = __shfl_up(v, off, kWave);
-        if (threadIdx.x % kWave >= off) v += o;
-    }
+    const double v = wave_scan(mine);
     if (threadIdx.x % kWave == kWave - 1) red[threadIdx.x / kWave] = v;
     __syncthreads();
     double before = 0.0, sum = 0.0;
@@ -79,13 +94,9 @@ __device__ inline double block_scan(double mine, double* red, double* all) {
 }
 
 __device__ inline double block_sum(double v, double* red) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
-    __syncthreads();
-    const double s = ((red[0] + red[1]) + red[2]) + red[3];
-    __syncthreads();
-    return s;
+    double all;
+    block_scan(v, red, &all);
+    return all;
 }
 
 __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
@@ -138,7 +149,8 @@ __global__ __launch_bounds__(kThreads) void verify_walk_kernel(VerifyArgs A) {
                 const float my_p = child ? pt[i] : 0.0f, my_u = child ? uu[i] : 0.0f;
                 for (uint64_t m = __ballot(child); m; m &= m - 1) {
                     const int l = __ffsll((unsigned long long)m) - 1;
-                    const double pc = (double)__shfl(my_p, l, kWave), uc = (double)__shfl(my_u, l, kWave);
+                    const double pc = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_p), l));
+                    const double uc = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_u), l));
                     const bool take = A.d ? pc >= 0.0 : uc * rest < pc;
                     if (take) {
                         cur = b + l;
@@ -201,16 +213,15 @@ __device__ inline double scan_pieces(const double (&s)[kPieces], double* red, do
     return all;
 }
 
-// The least `first` and the greatest `last` over the threads (one LDS atomic per wave: 4096 on one address took 30 us)
-__device__ inline void first_and_last(int first, int last, int* at_first, int* at_last) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        first = min(first, __shfl_xor(first, off, kWave));
-        last = max(last, __shfl_xor(last, off, kWave));
-    }
+// The least `first` below `none` and the greatest `last` above -1 over the threads, both growing with the thread (one LDS
+// atomic per wave: 4096 on one address took 30 us)
+__device__ inline void first_and_last(int first, int none, int last, int* at_first, int* at_last) {
+    const uint64_t f = __ballot(first < none), l = __ballot(last >= 0);
+    const int lo = f ? __builtin_amdgcn_readlane(first, __builtin_ctzll(f)) : none;
+    const int hi = l ? __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(l)) : -1;
     if (threadIdx.x % kWave == 0) {
-        atomicMin(at_first, first);
-        atomicMax(at_last, last);
+        if (f) atomicMin(at_first, lo);
+        if (l) atomicMax(at_last, hi);
     }
 }
 
@@ -267,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs A) {
             some = tid * per + k;
             if (before[k] + s[k] > goal) past = min(past, some);
         }
-    first_and_last(past, some, &s_piece, &s_some);
+    first_and_last(past, A.pieces, some, &s_piece, &s_some);
     __syncthreads();
     const int piece = s_piece < A.pieces ? s_piece : s_some;  // (no piece reaches the goal: the last with any weight)
 #pragma unroll
@@ -304,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs A) {
             if (c > goal) found = min(found, positive);
         }
     }
-    first_and_last(found, positive, &s_found, &s_positive);
+    first_and_last(found, kPiece, positive, &s_found, &s_positive);
     __syncthreads();
     // (a piece whose entries sum to a little less here than in the other order: its last entry)
     if (tid == 0) A.next[seq] = base + (s_found < kPiece ? s_found : max(s_positive, 0));
