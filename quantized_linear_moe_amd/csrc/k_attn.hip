@@ -490,8 +490,9 @@ struct Tiles {
     }
 };
 
-// Workgroup -> key head (fastest, so that a head's tiles meet in one L2), tile of rows (the last, longest one first),
-// sequence, piece
+// Workgroup -> key head (fastest, so that a head's tiles meet in one L2), tile of rows (the last, longest one first), piece,
+// sequence (pieces last would leave the pieces that only long sequences have to the end: 8 trees of 8 to 48 tokens over
+// 1100 to 4000 keys, 8-bit cache: 52 us in place of 39 with 6 pieces; trees and lengths all alike: no difference)
 template <int HD, int NW, bool I8, bool kRuns>
 __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     constexpr int BK = 64, NT = NW * kWave, TILE = BK * HD * 2;
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
     id /= A.n_kv;
     const int tile = A.row_tiles - 1 - id % A.row_tiles;
     id /= A.row_tiles;
-    const int seq = id % A.n_seq, split = id / A.n_seq, lo = split * A.chunk;
+    const int split = id % A.splits, seq = id / A.splits, lo = split * A.chunk;
     Tiles<HD, BK, NT, I8, kRuns> tiles;
     tiles.early(A, seq, lo);
     const Seq q = seq_of(A, seq);
@@ -826,24 +827,30 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 //   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads, 8-bit
 //   cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
 //   Many rows: no more than pay.  A piece's rows are written and read back as float32 (8 bytes a channel at the copy
-//   rate), and 64 keys take a workgroup 1.1 us, so that pieces cost `join` each and leave tiles * 1.1 / pieces to wait for,
-//   least at the root of their quotient (8 trees of 48 tokens, 28 heads, 4000 keys: 52 us with 6 pieces, 54 with 4,
-//   60 with 10; one tree: 18 us with 16, 21 with 8).  A sequence much longer than the others is still shared by 256
-//   workgroups, or in pieces of 8192 keys.
+//   rate), 64 keys take a workgroup 2 us where two share a CU, and the join's launch 6: pieces cost `join` each and leave
+//   whole / pieces to wait for, least at the root of their quotient.  Where every sequence has rows for all its row tiles,
+//   no more than run at once, 2 per CU; where some have not, the call's tokens bound the workgroups that have work, their
+//   lengths are unlike, and more of them even the CUs out (4000 keys, 28 heads, 8 trees of 48 tokens: 49 us with 5 pieces,
+//   54 with 6, 60 with 7; 16 of 8 to 20 tokens with 64 heads: 59 with 5, 77 with 4; 8 of 8 to 48, 8-bit cache: 34 with
+//   8, 39 with 6).  A sequence much longer than the others is still shared by 256 workgroups, or in pieces of 8192 keys.
 AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int max_q, int max_kv) {
     AttnPlan P;
     const long group = n_heads / cache->n_kv_heads, rows = max_q * group;
     P.few_rows = rows <= 32;
     P.row_tiles = P.few_rows ? 1 : (int)((rows + 127) / 128);
-    const long base = (long)n_seq * cache->n_kv_heads * P.row_tiles;
+    // workgroups with rows: every sequence's last tile may be a partial one
+    const long tiles = (long)n_seq * P.row_tiles, filled = std::min(tiles, T * group / 128 + n_seq);
+    const long base = cache->n_kv_heads * filled;
     const bool i8 = cache->dtype == QE_I8, narrow = cache->head_dim == 64;
-    const long at_once = !P.few_rows ? 640 : i8 ? (narrow ? 768 : 512) : narrow ? 512 : 256;
+    const long at_once = !P.few_rows ? (filled < tiles ? 720 : 512) : i8 ? (narrow ? 768 : 512) : narrow ? 512 : 256;
     long pieces = std::min(at_once / base, (max_kv + 127) / 128L);
     if (P.few_rows && at_once < 2 * base)
         pieces = std::min(((at_once > 256 ? 4 : 2) * at_once + base - 1) / base, max_kv / 512L);
     if (!P.few_rows) {
         const double join = std::min((double)n_seq * max_q, (double)T) * n_heads * cache->head_dim * 8 / 5e6;  // us
-        pieces = std::min(pieces, std::lround(std::sqrt(max_kv / 64 * 1.1 / join)));
+        const double whole = max_kv / 64.0 * 2.0;
+        pieces = std::max(1L, std::min(pieces, std::lround(std::sqrt(whole / join))));
+        if (whole / pieces + pieces * join + 6.0 > whole) pieces = 1;
     }
     const long alone = (long)cache->n_kv_heads * P.row_tiles;  // workgroups of one sequence
     pieces = std::max({pieces, std::min((max_kv + 8191) / 8192L, (255 + alone) / alone), 1L});
