@@ -430,7 +430,7 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
  *   sequence's keys p * page_size and on.  max_q, max_kv: no sequence has more new tokens or keys (what exceeds them
  *   is left out); they choose the launch, so that a captured call serves every length up to them.
  *   Lengths past max_pages * page_size are cut to it, keys of pages outside the cache are not seen, and what lies in
- *   places past kv_len is not read, so it may be anything; keys and values before that are finite.
+ *   places past kv_len is not read.  What a token does not see does not reach its row, infinities and NaN included.
  *   Products on the matrix cores with float32 sums, maxima and sums of the softmax in float32, its weights rounded to
  *   bf16 (QE_I8: after their values' scales) for the second product.  Deterministic.
  *   head_dim 64 or 128 (else QE_ERR_UNSUPPORTED), n_heads a multiple of n_kv_heads, max_kv at most 2^30, scale > 0.

@@ -9,16 +9,17 @@
 //   2^(s - m) are at most 2^8, which costs no precision in a floating-point sum;
 //   l' = l 2^(m - m') + sum_j 2^(s_j - m'), o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j, all in float32
 //
-// The weights are rounded to bf16 for the matrix cores (at most 2^-8 relative each, as the values they multiply were); l is summed
-// from the rounded weights (8-bit cache: from the unrounded ones, as the values' scales go into the weights), so
-// that what is divided by is the sum of what was multiplied.
+// The weights are rounded to bf16 for the matrix cores (at most 2^-8 relative each, as the values they multiply were); l
+// is summed from the rounded weights, so that what is divided by is the sum of what was multiplied (8-bit cache: from the
+// unrounded ones, as the values' scales go into the weights).
 //
 // Rows of a sequence and key head are its tokens times its group of query heads.  Two forms:
 //   many rows: a wave has 32 rows, the waves of a workgroup share tiles of 64 keys
 //   few rows (at most 32): every wave has them all, and its own tiles of 32 keys in turn; the waves' results join in LDS
 // Long sequences of few workgroups are split into pieces of `chunk` keys whose unnormalised results join in a second
 // kernel, in order.  Keys past the sequence or of a page outside the cache are never read: their rows come from a zero
-// constant, so that whatever those places hold stays out of the products.
+// constant, so that whatever those places hold stays out of the products; of keys that only some rows see (later ones, other
+// branches) neither scores nor values reach the other rows.
 #include <algorithm>
 #include <cmath>
 
@@ -33,6 +34,7 @@ namespace {
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef uint16_t v2us __attribute__((ext_vector_type(2)));
 
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
@@ -337,8 +339,53 @@ __device__ inline void attn_rescale(float mx, float sc, Rows<HD>& R) {
     }
 }
 
-// Weights of the scores and their products with V
-template <int HD, int NS, bool I8>
+// Whether so many bytes of values hold an infinity or a NaN
+template <int BYTES>
+__device__ inline bool attn_unbounded(const uint8_t* vbuf) {
+    v2us top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < BYTES / (kWave * 16); ++i) {
+        const v4u w = *reinterpret_cast<const v4u*>(vbuf + (i * kWave + threadIdx.x % kWave) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(v2us, w[e] & 0x7fff7fffu));
+    }
+    return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
+}
+
+// The products of such a tile, a key at a time: what a weight of zero belongs to is left out (the matrix cores would make
+// a NaN of 0 x infinity, in rows that do not see the key)
+template <int HD, int NS>
+__device__ inline void attn_values_each(const uint8_t* vbuf, const v8bf (&p)[NS][2], Rows<HD>& R) {
+    const int lane = threadIdx.x % kWave, h = lane / 32;
+    for (int j = 0; j < 32 * NS; ++j) {
+        const int at = (j >> 5) * 8 + ((j >> 3) & 3) * 2 + ((j >> 1) & 1);  // of the pair of weights with key j's
+        uint32_t u = 0;
+#pragma unroll
+        for (int b = 0; b < NS; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (8 * b + 4 * e + i == at) u = __builtin_bit_cast(v4u, p[b][e])[i];
+        const float w = __shfl(__uint_as_float(j & 1 ? u & 0xffff0000u : u << 16), lane % 32 + ((j >> 2) & 1) * 32, kWave);
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int piece = (4 * d + a) ^ v_swizzle<HD>(j);
+                const v2u x = *reinterpret_cast<const v2u*>(vbuf + j * HD * 2 + (piece << 4) + 8 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+                    R.o[d][4 * a + e] = w == 0.0f ? R.o[d][4 * a + e] : __builtin_fmaf(w, v, R.o[d][4 * a + e]);
+                }
+            }
+    }
+}
+
+// Weights of the scores and their products with V.  kMasked: some rows may not see all the tile's keys, and what those
+// hold, infinities and NaN too, must not reach them (looking for those takes 1 us of a call with a tile of 64 to mask)
+template <int HD, int NS, bool I8, bool kMasked>
 __device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float sc, const v16f (&s)[NS], Rows<HD>& R) {
     const int lane = threadIdx.x % kWave, h = lane / 32;
     v8bf p[NS][2];
@@ -354,7 +401,7 @@ __device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float 
             for (int a = 0; a < 4; ++a) {
                 const v4f f = *reinterpret_cast<const v4f*>(vsb + 32 * b + 8 * a + 4 * h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[4 * a + i] *= f[i];
+                for (int i = 0; i < 4; ++i) w[4 * a + i] = kMasked && w[4 * a + i] == 0.0f ? 0.0f : w[4 * a + i] * f[i];
             }
         }
 #pragma unroll
@@ -371,6 +418,12 @@ __device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float 
                 u[i] = __builtin_bit_cast(uint32_t, pk);
             }
             p[b][e] = __builtin_bit_cast(v8bf, u);
+        }
+    }
+    if constexpr (kMasked && !I8) {
+        if (__builtin_expect(attn_unbounded<NS * 32 * HD * 2>(vbuf), 0)) {
+            attn_values_each<HD, NS>(vbuf, p, R);
+            return;
         }
     }
     // V^T: lane l reads 4 keys of channel l % 32 at a time, through its group of 16 lanes
@@ -568,7 +621,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
             begin();
             attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
             attn_rescale(attn_max<2>(s), A.sc, R);
-            attn_values<HD, 2, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
+            attn_values<HD, 2, I8, false>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
         // a wave without rows only loads (64 sequences of 8 tokens over 512 to 8000 keys, 64 heads: 278 -> 257 us); every
@@ -584,7 +637,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
             attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
             attn_mask<2>(seen, s);
             attn_rescale(attn_max<2>(s), A.sc, R);
-            attn_values<HD, 2, I8>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
+            attn_values<HD, 2, I8, true>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
     }
@@ -682,7 +735,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
             begin();
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb, A.sc, s, R);
+            attn_values<HD, 1, I8, false>(vbuf + buf * TILE, vsb, A.sc, s, R);
             end();
         }
         while (k0 < hi) {
@@ -691,7 +744,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_mask<1>(seen, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8>(vbuf + buf * TILE, vsb, A.sc, s, R);
+            attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R);
             end();
         }
     }
@@ -830,8 +883,8 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 // How many pieces: as many as fill the workgroups that run at once (few rows: 1 to 3 per CU, by LDS and registers; many
 // rows: two, and some more, as sequences differ), of 128 keys or more.
 //   Few rows, as many sequences and heads as run at once already: pieces for two rounds (where several workgroups share a
-//   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads, 8-bit
-//   cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
+//   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads,
+//   8-bit cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
 //   Many rows: no more than pay.  A piece's rows are written and read back as float32 (8 bytes a channel at the copy
 //   rate), 64 keys take a workgroup 2 us where two share a CU, and the join's launch 6: pieces cost `join` each and leave
 //   whole / pieces to wait for, least at the root of their quotient.  Where every sequence has rows for all its row tiles,

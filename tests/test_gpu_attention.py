@@ -194,6 +194,54 @@ def test_tokens_that_see_nothing(L):
     b.check(b.run(L))
 
 
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("lens", [[(3, 3)], [(6, 200)], [(20, 25), (9, 140)], [(70, 90), (41, 700)]])
+def test_infinities_and_nan_stay_with_the_rows_that_see_them(L, lens, tree, hd, i8):
+    """A later token's key and value, or another branch's, may be anything: the rows that do not see it keep theirs."""
+    tree = _forest(np.random.default_rng(7), lens, blank=0.2) if tree else None
+    b = Batch(L, lens, 4, 2, hd, 8, i8, tree=tree, seed=11)
+    for s, (n, length) in enumerate(lens):
+        for token, of, channel, value in ((n // 2, 1, 3, float("inf")), (n // 2 + 1, 1, 5, float("nan")),
+                                          (n - 1, 0, 7, float("nan")), (n - 1, 1, 9, float("-inf"))):
+            j = length - n + token
+            page, place = int(b.pages[s, j // 8]), j % 8
+            if i8:
+                (b.ks, b.vs)[of][page, :, place] = value
+            else:
+                (b.k, b.v)[of][page, :, place, channel] = value
+    for t, x in zip(b.tensors, (b.k, b.v, b.ks, b.vs)):
+        if x is not None:
+            t.copy_(x)
+    out = b.run(L)
+    got = out.float().cpu().numpy().astype(np.float64)
+    finite = 0
+    for s, (n, length) in enumerate(lens):
+        a = b.starts[s]
+        seen = C.sees(n, length - n, length, None if tree is None else tree[a:a + n])
+        with np.errstate(invalid="ignore"):
+            o = C.attention(b.q[a:a + n].float().cpu().numpy(), *b.keys_of(s, length), seen, hd ** -0.5)[0]
+        ok = np.isfinite(o)
+        finite += ok.sum()
+        assert np.array_equal(np.isfinite(got[a:a + n]), ok)
+        got[a:a + n][~ok] = 0
+    assert finite > 0
+    # what is finite, against a cache in which those places are zeros
+    for x in (b.k, b.v, b.ks, b.vs):
+        if x is not None and x.dtype != torch.int8:
+            x.nan_to_num_(0.0, 0.0, 0.0)
+    for s, (n, length) in enumerate(lens):
+        a = b.starts[s]
+        seen = C.sees(n, length - n, length, None if tree is None else tree[a:a + n])
+        o, A, reach = C.attention(b.q[a:a + n].float().cpu().numpy(), *b.keys_of(s, length), seen, hd ** -0.5)
+        d = hd ** -0.5 * reach * ((hd + 1) * 2.0 ** -23 + 8 * 2.0 ** -24) * 2
+        tol = 2.0 ** -8 * np.abs(o) + (1 + 2.0 ** -8) * A * (2 * 2.0 ** -8 + 2 * np.expm1(d) + 2.0 ** -20 +
+                                                             2 * seen.sum(1)[:, None, None] * 2.0 ** -23)
+        ok = np.isfinite(out.float().cpu().numpy()[a:a + n])
+        assert np.all((np.abs(got[a:a + n] - o) <= tol)[ok])
+
+
 def test_empty_and_short_sequences(L):
     """No new tokens, no keys at all, fewer keys than new tokens (the first ones' are missing)."""
     for n in (1, 5, 40):
