@@ -20,6 +20,15 @@
 // kernel, in order.  Keys past the sequence or of a page outside the cache are never read: their rows come from a zero
 // constant, so that whatever those places hold stays out of the products; of keys that only some rows see (later ones, other
 // branches) neither scores nor values reach the other rows.
+//
+// Bounds.  A prompt: the matrix cores, by power.  4096 tokens, 64 heads on 8 key heads of 128 channels: 285 us, 0.97 PFLOP/s
+// (a large bf16 product: 1.15 to 1.26); the matrix cores are busy 46 % of the cycles at 1.9 GHz, and taking out a part of
+// any of the loop's work (products, exponentials, LDS reads, copies) shortens it in proportion to that part.  Tiles of 64
+// keys in two buffers and 4 waves leave room for two workgroups per CU, of which one computes while the other waits (one per
+// CU: 362 us; 8 waves: +3 %; scores a tile ahead in the same wave: +1 % or spills).
+// Single tokens: memory.  64 sequences of 512 to 8192 keys: 210 us, 5.4 TB/s of the cache's bytes.
+// Trees: rows that fill no tile of 128, the pieces' unlike ends and the join.  8 trees of 7 to 48 tokens over up to 4000
+// keys, 28 heads on 4, 8-bit cache: 27 us and 5 to 6 of the join.
 #include <algorithm>
 #include <cmath>
 
@@ -544,7 +553,7 @@ struct Tiles {
 };
 
 // Workgroup -> key head (fastest, so that a head's tiles meet in one L2), tile of rows (the last, longest one first), piece,
-// sequence (pieces last would leave the pieces that only long sequences have to the end: 8 trees of 8 to 48 tokens over
+// sequence (pieces last would leave the pieces that only long sequences have to the end: 8 trees of 7 to 48 tokens over
 // 1100 to 4000 keys, 8-bit cache: 52 us in place of 39 with 6 pieces; trees and lengths all alike: no difference)
 template <int HD, int NW, bool I8, bool kRuns>
 __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
@@ -890,7 +899,7 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 //   whole / pieces to wait for, least at the root of their quotient.  Where every sequence has rows for all its row tiles,
 //   no more than run at once, 2 per CU; where some have not, the call's tokens bound the workgroups that have work, their
 //   lengths are unlike, and more of them even the CUs out (4000 keys, 28 heads, 8 trees of 48 tokens: 49 us with 5 pieces,
-//   54 with 6, 60 with 7; 16 of 8 to 20 tokens with 64 heads: 59 with 5, 77 with 4; 8 of 8 to 48, 8-bit cache: 34 with
+//   54 with 6, 60 with 7; 16 of 8 to 20 tokens with 64 heads: 59 with 5, 77 with 4; 8 of 7 to 48, 8-bit cache: 34 with
 //   8, 39 with 6).  A sequence much longer than the others is still shared by 256 workgroups, or in pieces of 8192 keys.
 AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int max_q, int max_kv) {
     AttnPlan P;

@@ -11,6 +11,11 @@
 // drawn token.  Only one row of p (and of the drafts') per sequence is read whole, the one where the walk ends; so the
 // first kernel's workgroups (one per sequence and piece of the vocabulary) each walk for themselves, from the rows'
 // gathered probabilities in LDS, then sum their piece; the second kernel finds the piece and the token in it.
+//
+// Bound by the chain of trips to memory (rows, tokens, probabilities, the last row, its sums, the piece): a chain of 5 rows
+// over 32000 entries 7.4 + 8.1 us, 32 trees of 33 rows over 131072 11.3 + 9.0 (17 MB of rows, 3 us at the copy rate).  One
+// kernel with a workgroup per sequence saves the second launch but reads a row on one CU: 11 us in place of 14 at 8000
+// entries, the same at 32000, 38 in place of 17 at 131072.
 #include <algorithm>
 
 #include "qe_cache.h"
