@@ -395,7 +395,8 @@ __device__ inline void attn_values_each(const uint8_t* vbuf, const v8bf (&p)[NS]
 // Weights of the scores and their products with V.  kMasked: some rows may not see all the tile's keys, and what those
 // hold, infinities and NaN too, must not reach them (looking for those takes 1 us of a call with a tile of 64 to mask)
 template <int HD, int NS, bool I8, bool kMasked>
-__device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float sc, const v16f (&s)[NS], Rows<HD>& R) {
+__device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float sc, const v16f (&s)[NS], Rows<HD>& R,
+                                   bool look = true) {
     const int lane = threadIdx.x % kWave, h = lane / 32;
     v8bf p[NS][2];
 #pragma unroll
@@ -430,7 +431,7 @@ __device__ inline void attn_values(const uint8_t* vbuf, const float* vsb, float 
         }
     }
     if constexpr (kMasked && !I8) {
-        if (__builtin_expect(attn_unbounded<NS * 32 * HD * 2>(vbuf), 0)) {
+        if (look && __builtin_expect(attn_unbounded<NS * 32 * HD * 2>(vbuf), 0)) {
             attn_values_each<HD, NS>(vbuf, p, R);
             return;
         }
@@ -704,6 +705,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
     RowMask mask;
     mask.init(A, q, row);
     const int all = q.ctx + (A.tree ? 0 : 1);
+    const bool differ = A.tree || q.n > 1;  // rows may: of one token's, all see what there is
 
     uint8_t* mine = smem + wave * REGION;
     float* scales = scales_all + (I8 ? wave * 2 * BK : 0);
@@ -753,7 +755,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_mask<1>(seen, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R);
+            attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R, differ);
             end();
         }
     }
@@ -891,6 +893,8 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 
 // How many pieces: as many as fill the workgroups that run at once (few rows: 1 to 3 per CU, by LDS and registers; many
 // rows: two, and some more, as sequences differ), of 128 keys or more.
+//   Few rows, up to 384 keys: one, as the join costs what two or three tiles do (12 heads on 2, one sequence: 256 keys 6.3
+//   us, in two pieces 7.8; 384 keys 7.3 and 7.9; 512 keys 8.2, in four 8.0).
 //   Few rows, as many sequences and heads as run at once already: pieces for two rounds (where several workgroups share a
 //   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads,
 //   8-bit cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
@@ -912,6 +916,7 @@ AttnPlan attn_plan(const qe_kv_cache* cache, int n_heads, int T, int n_seq, int 
     const bool i8 = cache->dtype == QE_I8, narrow = cache->head_dim == 64;
     const long at_once = !P.few_rows ? (filled < tiles ? 720 : 512) : i8 ? (narrow ? 768 : 512) : narrow ? 512 : 256;
     long pieces = std::min(at_once / base, (max_kv + 127) / 128L);
+    if (P.few_rows && max_kv <= 384) pieces = 1;
     if (P.few_rows && at_once < 2 * base)
         pieces = std::min(((at_once > 256 ? 4 : 2) * at_once + base - 1) / base, max_kv / 512L);
     if (!P.few_rows) {
