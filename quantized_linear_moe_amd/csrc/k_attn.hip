@@ -246,10 +246,12 @@ struct Stage {
     }
 };
 
-// Every copy of this wave has landed (rows of bf16), and its LDS writes are ordered before what follows
+// Every copy of this wave has landed (rows of bf16), and its reads of the tile at hand are done: in attn_keys_kernel, whose
+// waves meet no barrier, the next copies go where that tile lies
 template <bool I8>
 __device__ inline void landed() {
-    if constexpr (!I8) QE_WAIT_VMCNT(0);
+    asm volatile("" ::: "memory");  // (no read moves behind the wait)
+    if constexpr (!I8) QE_WAIT_VMCNT_LDS(0);
     asm volatile("" ::: "memory");
 }
 
