@@ -427,10 +427,11 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
  *   q, out: device bf16 [T][n_heads][head_dim], tokens q_stride and out_stride elements apart; no overlap.
  *   q_start: device int32 [n_seq + 1], ascending from 0 on, at most T; rows of out behind the last sequence are left as
  *   they were.  kv_len: device int32 [n_seq].  pages: device int32 [n_seq][max_pages], entry p the page of the
- *   sequence's keys p * page_size and on.  max_q, max_kv: no sequence has more new tokens or keys (what exceeds them
- *   is left out); they choose the launch, so that a captured call serves every length up to them.
- *   Lengths past max_pages * page_size are cut to it, keys of pages outside the cache are not seen, and what lies in
- *   places past kv_len is not read.  What a token does not see does not reach its row, infinities and NaN included.
+ *   sequence's keys p * page_size and on.  max_q, max_kv: no sequence has more new tokens or keys; they choose the
+ *   launch, so that a captured call serves every length up to them.
+ *   What exceeds the bounds is left out: tokens past max_q get no row, keys past max_kv or max_pages * page_size are not
+ *   seen, and the others are what they are (the new tokens' own keys are the last n of kv_len, also where some of those
+ *   are left out).  Keys of pages outside the cache are not seen, and what lies in places past kv_len is not read.  What a token does not see does not reach its row, infinities and NaN included.
  *   Products on the matrix cores with float32 sums, maxima and sums of the softmax in float32, its weights rounded to
  *   bf16 (QE_I8: after their values' scales) for the second product.  Deterministic.
  *   head_dim 64 or 128 (else QE_ERR_UNSUPPORTED), n_heads a multiple of n_kv_heads, max_kv at most 2^30, scale > 0.

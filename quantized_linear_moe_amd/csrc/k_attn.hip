@@ -67,9 +67,10 @@ struct AttnArgs {
     float2* part_ml;
 };
 
-// A sequence's new tokens [first, first + n) and keys (clamped to what the arguments allow)
+// A sequence's new tokens [first, first + n) and keys (clamped to what the arguments allow).  Which keys the new tokens are
+// goes by the length as given: what the bounds cut off is missing, and nothing else moves.
 struct Seq {
-    int first, n, len, ctx;  // ctx: keys before the new tokens (may be negative)
+    int first, n, len, ctx;  // ctx: keys before the new tokens, at most len (may be negative)
 };
 __device__ inline Seq seq_of(const AttnArgs& A, int s) {
     Seq q;
@@ -77,8 +78,9 @@ __device__ inline Seq seq_of(const AttnArgs& A, int s) {
     const int n = min(max(A.q_start[s + 1], q.first), A.T) - q.first;
     q.n = min(n, A.max_q);
     const long cap = min((long)A.max_kv, (long)A.max_pages << A.page_shift);
-    q.len = (int)min((long)max(A.kv_len[s], 0), cap);
-    q.ctx = q.len - n;
+    const int given = max(A.kv_len[s], 0);
+    q.len = (int)min((long)given, cap);
+    q.ctx = min(given - n, q.len);  // (ctx + n is at most given: 31 bits)
     return q;
 }
 

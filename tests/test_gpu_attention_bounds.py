@@ -1,0 +1,55 @@
+"""Attention past the bounds that a call names, over long pieces, and of values near the end of their range; against the
+definition in float64, with the bound of test_gpu_attention.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attention import BF, DEV, Batch, _forest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from quantized_linear_moe_amd import libqe
+    return libqe
+
+
+def _i32(a):
+    return torch.tensor(a, dtype=torch.int32, device=DEV)
+
+
+def _first(cut):
+    """Only the first cut keys are there."""
+    def seen_of(s, seen):
+        seen = seen.copy()
+        seen[:, cut:] = False
+        return seen
+    return seen_of
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("n,length,cut", [(2, 100, 98), (2, 100, 99), (3, 64, 32), (7, 700, 640), (10, 100, 90), (60, 60, 16),
+                                          (60, 300, 256), (40, 1000, 976), (33, 100, 48)])
+def test_keys_past_the_bounds_are_left_out(L, n, length, cut, tree, i8):
+    """The new tokens are the last of kv_len keys whatever max_kv and the page table keep of them."""
+    lens = [(n, length), (n, length)]
+    bits = _forest(np.random.default_rng(n + cut), lens) if tree else None
+    b = Batch(L, lens, 8, 2, 64, 16, i8, tree=bits, seed=n, tail=1)
+    b.check(b.run(L, max_kv=cut), seen_of=_first(cut))
+    cut -= cut % 16
+    b.pages_dev = b.pages[:, :cut // 16].contiguous().to(DEV)
+    b.check(b.run(L), seen_of=_first(cut))
+
+
+@pytest.mark.parametrize("n", [1, 3, 50])
+def test_lengths_far_past_the_bounds(L, n):
+    """Every key that there is lies before the new tokens."""
+    for tree in (None, _forest(np.random.default_rng(n), [(n, 112)])):
+        b = Batch(L, [(n, 112)], 4, 2, 64, 16, tree=tree, seed=n)
+        for length in (2 ** 31 - 1, 2 ** 30, 112 + n):
+            b.kv_len = _i32([length])
+            for max_kv in (112, 4000, 2 ** 30):
+                b.check(b.run(L, max_kv=max_kv), seen_of=lambda s, seen: np.ones_like(seen))
