@@ -709,7 +709,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
     RowMask mask;
     mask.init(A, q, row);
     const int all = q.ctx + (A.tree ? 0 : 1);
-    const bool differ = A.tree || q.n > 1;  // rows may: of one token's, all see what there is
+    const bool hidden = A.tree || all < q.len;  // there may be keys that some rows do not see
 
     uint8_t* mine = smem + wave * REGION;
     float* scales = scales_all + (I8 ? wave * 2 * BK : 0);
@@ -759,7 +759,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_mask<1>(seen, s);
             attn_rescale(attn_max<1>(s), A.sc, R);
-            attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R, differ);
+            attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R, hidden);
             end();
         }
     }

@@ -53,3 +53,24 @@ def test_lengths_far_past_the_bounds(L, n):
             b.kv_len = _i32([length])
             for max_kv in (112, 4000, 2 ** 30):
                 b.check(b.run(L, max_kv=max_kv), seen_of=lambda s, seen: np.ones_like(seen))
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n", [2, 5, 40])
+def test_infinities_behind_the_tokens_that_max_q_keeps(L, n, i8):
+    """The keys of the tokens that are left out stay unseen, whatever they hold."""
+    for keep in (1, n - 1):
+        b = Batch(L, [(n, 90)], 4, 2, 64, 16, i8, seed=n)
+        full = b.run(L)
+        for j in range(90 - n + keep, 90):
+            page, place = int(b.pages[0, j // 16]), j % 16
+            for x, value in zip((b.ks, b.vs) if i8 else (b.k, b.v), (float("nan"), float("inf"))):
+                x[page, :, place] = value
+        for t, x in zip(b.tensors, (b.k, b.v, b.ks, b.vs)):
+            if x is not None:
+                t.copy_(x)
+        out = b.run(L, max_q=keep)
+        assert bool((out[keep:] == 77).all()) and bool(torch.isfinite(out[:keep]).all())
+        # the same keys; another launch may sum them in another order, each within its bound of 2^-6 sum p |v|
+        top = 127 * float(b.vs[torch.isfinite(b.vs)].max()) if i8 else float(b.v[torch.isfinite(b.v)].abs().max())
+        assert float((out[:keep].float() - full[:keep].float()).abs().max()) <= 2.0 ** -5 * top
