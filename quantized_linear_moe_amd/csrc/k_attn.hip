@@ -5,9 +5,12 @@
 // tile (the maximum), its weights are the B operand of O^T = V^T P^T as they lie (V^T is read from LDS in the same key
 // order by transposing reads), and the running factors of O^T are per lane.
 //
-//   m' = max(m, max_j s_j), taken over only when it exceeds m by 8 (in units of log2): until then the weights
-//   2^(s - m) are at most 2^8, which costs no precision in a floating-point sum;
+//   m' = max(m, c + max_j s_j), taken over only when it exceeds m by 8 (in units of log2);
 //   l' = l 2^(m - m') + sum_j 2^(s_j - m'), o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j, all in float32
+//
+// with c = 8 + the bits of the number of keys, so that a weight is at most 2^(8 - c) and all of them at most 1 together:
+// o stays within the values' own range, whatever it is.  The exponent s - m' is then off by up to c 2^-24 (1.3e-6 at 8192
+// keys), little beside the weights' rounding to bf16 (2^-8).
 //
 // The weights are rounded to bf16 for the matrix cores (at most 2^-8 relative each, as the values they multiply were); l
 // is summed from the rounded weights, so that what is divided by is the sum of what was multiplied (8-bit cache: from the
@@ -47,6 +50,7 @@ typedef uint16_t v2us __attribute__((ext_vector_type(2)));
 
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLazy = 8.0f;
+__device__ inline float lift_of(int keys) { return kLazy + (float)(32 - __builtin_clz(max(keys, 1))); }  // c above
 
 __device__ __attribute__((aligned(16))) const uint32_t kZero16[4] = {0, 0, 0, 0};
 
@@ -339,10 +343,10 @@ __device__ inline float attn_max(const v16f (&s)[NS]) {
     return mx;
 }
 
-// The running maximum moves where the scores (their greatest in this lane: mx) exceed it by far
+// The running maximum (with lift_of on it) moves where the scores (their greatest in this lane: mx) exceed it by far
 template <int HD>
-__device__ inline void attn_rescale(float mx, float sc, Rows<HD>& R) {
-    mx = half_max(mx) * sc;
+__device__ inline void attn_rescale(float mx, float sc, float lift, Rows<HD>& R) {
+    mx = half_max(mx) * sc + lift;
     if (__any(mx > R.m + kLazy)) {
         const float m = fmaxf(R.m, mx), f = __builtin_amdgcn_exp2f(R.m - m);
         R.m = m;
@@ -593,6 +597,8 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
         seen[1] = (uint32_t)(valid >> 32) & mask.of(k0 + 32 - q.ctx);
     };
 
+    const float lift = lift_of(q.len);
+
     uint8_t *kbuf = smem, *vbuf = smem + 2 * TILE;
     float *ksb = scales, *vsb = scales + 2 * BK;
     const uint32_t klds = lds_addr(kbuf), vlds = lds_addr(vbuf);
@@ -634,7 +640,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
         while (k0 < hi && k0 + BK <= all && t.whole) {
             begin();
             attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
-            attn_rescale(attn_max<2>(s), A.sc, R);
+            attn_rescale(attn_max<2>(s), A.sc, lift, R);
             attn_values<HD, 2, I8, false>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
@@ -650,7 +656,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
             begin();
             attn_scores<HD, 2, I8>(kbuf + buf * TILE, ksb + buf * BK, R, s);
             attn_mask<2>(seen, s);
-            attn_rescale(attn_max<2>(s), A.sc, R);
+            attn_rescale(attn_max<2>(s), A.sc, lift, R);
             attn_values<HD, 2, I8, true>(vbuf + buf * TILE, vsb + buf * BK, A.sc, s, R);
             end();
         }
@@ -711,6 +717,8 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
     const int all = q.ctx + (A.tree ? 0 : 1);
     const bool hidden = A.tree || all < q.len;  // there may be keys that some rows do not see
 
+    const float lift = lift_of(q.len);
+
     uint8_t* mine = smem + wave * REGION;
     float* scales = scales_all + (I8 ? wave * 2 * BK : 0);
     uint8_t *kbuf = mine, *vbuf = mine + BUFS * TILE;
@@ -749,7 +757,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
         while (k0 < hi && k0 + BK <= all && t.whole) {
             begin();
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
-            attn_rescale(attn_max<1>(s), A.sc, R);
+            attn_rescale(attn_max<1>(s), A.sc, lift, R);
             attn_values<HD, 1, I8, false>(vbuf + buf * TILE, vsb, A.sc, s, R);
             end();
         }
@@ -758,7 +766,7 @@ __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(
             begin();
             attn_scores<HD, 1, I8>(kbuf + buf * TILE, ksb, R, s);
             attn_mask<1>(seen, s);
-            attn_rescale(attn_max<1>(s), A.sc, R);
+            attn_rescale(attn_max<1>(s), A.sc, lift, R);
             attn_values<HD, 1, I8, true>(vbuf + buf * TILE, vsb, A.sc, s, R, hidden);
             end();
         }

@@ -74,3 +74,26 @@ def test_infinities_behind_the_tokens_that_max_q_keeps(L, n, i8):
         # the same keys; another launch may sum them in another order, each within its bound of 2^-6 sum p |v|
         top = 127 * float(b.vs[torch.isfinite(b.vs)].max()) if i8 else float(b.v[torch.isfinite(b.v)].abs().max())
         assert float((out[:keep].float() - full[:keep].float()).abs().max()) <= 2.0 ** -5 * top
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n,length", [(1, 2), (1, 300), (1, 3000), (3, 40), (40, 300), (33, 2000)])
+def test_values_near_the_end_of_their_range(L, n, length, i8):
+    """The sums of weighted values stay finite where the rows are: equal scores, and scores that grow along the keys."""
+    for steep in (0.0, 1.0):
+        b = Batch(L, [(n, length)], 4, 2, 64, 16, i8, seed=length)
+        j = torch.arange(length)
+        p, o = b.pages[0].long()[j // 16], j % 16
+        if i8:
+            b.vs[p, :, o] = 2.2e36
+            b.v.abs_()
+            b.ks[p, :, o] = (steep * j / length / 127)[:, None].expand(length, 2).contiguous()
+            b.k.fill_(127)
+        else:
+            b.v[p, :, o] = (2.9e38 * (1 - torch.rand(length, 2, 64, generator=torch.Generator().manual_seed(n)) / 8)).to(BF)
+            b.k[p, :, o] = (steep * j / length)[:, None, None].expand(length, 2, 64).to(BF)
+        b.q_rows.copy_(b.q_rows.abs())
+        for t, x in zip(b.tensors, (b.k, b.v, b.ks, b.vs)):
+            if x is not None:
+                t.copy_(x)
+        b.check(b.run(L))
