@@ -97,3 +97,62 @@ def test_values_near_the_end_of_their_range(L, n, length, i8):
             if x is not None:
                 t.copy_(x)
         b.check(b.run(L))
+
+
+def _long(L, form, i8, whole, seed, hd=64, tree=False):
+    """Two long sequences; whole: among so many short ones that keys are not divided."""
+    n, short = (1, 400) if form == "few" else (40, 80)
+    lens = [(n, 2300)] + [(1, 1 + s % 30) for s in range(short if whole else 0)] + [(n, 2049)]
+    bits = _forest(np.random.default_rng(seed), lens) if tree else None
+    b = Batch(L, lens, 8, 8, hd, 16, i8, tree=bits, seed=seed, tail=1)
+    pieces = L.qe_attention_workspace_bytes(b.cache, 8, b.T + 1, len(lens), n, 2300) > 0
+    assert pieces != whole
+    return b
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("form,tree", [("few", False), ("rows", False), ("rows", True)])
+@pytest.mark.parametrize("whole", [True, False])
+def test_long_pieces(L, whole, form, tree, hd, i8):
+    """More than 128 pages of 16 in one piece, and pages outside the cache among the first 64 and far behind."""
+    b = _long(L, form, i8, whole, 3, hd, tree)
+    b.check(b.run(L))
+    bad = [5, 63, 64, 70, 127, 128, 140]
+    pages = b.pages.clone()
+    for i, p in enumerate(bad):
+        pages[0, p] = (-1, b.k.shape[0], 2 ** 31 - 1, -2 ** 31)[i % 4]
+    b.pages_dev = pages.to(DEV)
+
+    def seen_of(s, seen):
+        seen = seen.copy()
+        for p in bad if s == 0 else []:
+            seen[:, p * 16:(p + 1) * 16] = False
+        return seen
+    b.check(b.run(L), seen_of=seen_of)
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("form", ["few", "rows"])
+@pytest.mark.parametrize("whole", [True, False])
+def test_keys_at_borders_count_once(L, whole, form, i8):
+    """Nearly all weight on keys beside the borders of tiles, waves, pieces and windows of pages, each a like share: one
+    left out or taken twice moves the row by a multiple of the bound."""
+    b = _long(L, form, i8, whole, 4)
+    for s, (n, length) in ((0, b.lens[0]), (len(b.lens) - 1, b.lens[-1])):
+        j = torch.arange(length)
+        p, o = b.pages[s].long()[j // 16], j % 16
+        at = torch.tensor(sorted({0, 31, 32, 63, 64, 127, 128, 255, 256, 511, 512, 1023, 1024, 1151, 1152, 2047, 2048,
+                                  length - 41, length - 1}))
+        f = torch.full((length,), 1e-3)
+        f[at] = 3.0
+        if i8:
+            b.k[p, :, o] = 127
+            b.ks[p, :, o] = (f / 127)[:, None].expand(length, 8).contiguous()
+        else:
+            b.k[p, :, o] = f[:, None, None].to(BF).expand(length, 8, 64)
+    b.q_rows.copy_(b.q_rows.abs())
+    for t, x in zip(b.tensors, (b.k, b.v, b.ks, b.vs)):
+        if x is not None:
+            t.copy_(x)
+    b.check(b.run(L))
