@@ -553,6 +553,8 @@ def qe_attention(cache: qe_kv_cache, q, q_start, kv_len, pages, max_q, max_kv, o
     pl = _arg(f, "kv_len", kv_len, (n,), torch.int32, dev)
     pp = _arg(f, "pages", pages, (n, pages.shape[-1]), torch.int32, dev)
     words = 0 if tree is None else tree.shape[-1]
+    if tree is not None and words == 0:  # (its address is NULL, which would read as no tree)
+        raise ValueError(f"{f}: tree has no words")
     pt = None if tree is None else _arg(f, "tree", tree, (T, words),
                                         torch.uint32 if tree.dtype is torch.uint32 else torch.int32, dev)
     pw = None if ws is None else _arg(f, "ws", ws, ws.shape, ws.dtype, dev)
