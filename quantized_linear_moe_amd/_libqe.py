@@ -481,6 +481,13 @@ def _rows(where, name, t, shape, index):
     raise ValueError(f"{where}: {name} is on {t.device}, not on device {index}")
 
 
+def _bound(where, name, n):
+    """A caller's count, which has to be an int32 (ctypes would cut off the bits above: of 2^32 keys, all)."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError(f"{where}: {name} must fit in 32 bits, got {n}")
+    return n
+
+
 def _pos(where, rope, pos, T, index):
     """The address of positions int32 [n_pos, T], or [T] for one row (and the frequencies are on their device)."""
     rows = rope.n_pos
@@ -535,6 +542,8 @@ def qe_kv_append(cache: qe_kv_cache, k, v, slot, rope=None, pos=None, q=None, q_
 
 
 def qe_attention_workspace_bytes(cache: qe_kv_cache, n_heads, T, n_seq, max_q, max_kv) -> int:
+    if max(max_q, max_kv) > 0x7FFFFFFF:  # (refused by the call; ctypes would cut off the bits above)
+        return 0
     return _lib.qe_attention_workspace_bytes(ctypes.byref(cache), n_heads, T, n_seq, max_q, max_kv)
 
 
@@ -558,8 +567,9 @@ def qe_attention(cache: qe_kv_cache, q, q_start, kv_len, pages, max_q, max_kv, o
     pt = None if tree is None else _arg(f, "tree", tree, (T, words),
                                         torch.uint32 if tree.dtype is torch.uint32 else torch.int32, dev)
     pw = None if ws is None else _arg(f, "ws", ws, ws.shape, ws.dtype, dev)
-    _call_on(dev, f, _lib.qe_attention, ctypes.byref(cache), pq, sq, T, h, p0, pl, pp, n, pages.shape[-1], max_q, max_kv,
-             pt, words, d ** -0.5 if scale is None else scale, po, so, pw, 0 if ws is None else ws.nbytes, stream=stream)
+    _call_on(dev, f, _lib.qe_attention, ctypes.byref(cache), pq, sq, T, h, p0, pl, pp, n, pages.shape[-1],
+             _bound(f, "max_q", max_q), _bound(f, "max_kv", max_kv), pt, words, d ** -0.5 if scale is None else scale, po, so,
+             pw, 0 if ws is None else ws.nbytes, stream=stream)
 
 
 def qe_verify_workspace_bytes(n_seq, vocab) -> int:
@@ -586,7 +596,7 @@ def qe_verify_drafts(p, row_start, token, u, taken, path, next, ws, draft_p=None
         ("u", u, (N,), torch.float32), ("taken", taken, (n,), i32), ("path", path, (N,), i32), ("next", next, (n,), i32),
         ("ws", ws, ws.shape, ws.dtype))]
     _call_on(dev, f, _lib.qe_verify_drafts, p.data_ptr(), strides[0], _ptr(draft_p), strides[1], V, a[0], N, a[1], a[2],
-             a[3], n, max_rows, a[4], a[5], a[6], a[7], ws.nbytes, stream=stream)
+             a[3], n, _bound(f, "max_rows", max_rows), a[4], a[5], a[6], a[7], ws.nbytes, stream=stream)
 
 
 def qe_colmean_abs(W, w, stream=None):
