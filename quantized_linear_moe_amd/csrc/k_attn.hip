@@ -24,14 +24,20 @@
 // constant, so that whatever those places hold stays out of the products; of keys that only some rows see (later ones, other
 // branches) neither scores nor values reach the other rows.
 //
-// Bounds.  A prompt: the matrix cores, by power.  4096 tokens, 64 heads on 8 key heads of 128 channels: 285 us, 0.97 PFLOP/s
-// (a large bf16 product: 1.15 to 1.26); the matrix cores are busy 46 % of the cycles at 1.9 GHz, and taking out a part of
-// any of the loop's work (products, exponentials, LDS reads, copies) shortens it in proportion to that part.  Tiles of 64
-// keys in two buffers and 4 waves leave room for two workgroups per CU, of which one computes while the other waits (one per
-// CU: 362 us; 8 waves: +3 %; scores a tile ahead in the same wave: +1 % or spills).
+// Bounds (kernel times of runs of 0.25 s; after a pause the first 50 or so large launches take up to a quarter more, until the
+// clock has settled).
+// A prompt: 4096 tokens, 64 heads on 8 key heads of 128 channels: 276 to 280 us, 0.98 to 1.0 PFLOP/s (a large bf16
+// product: 1.15 to 1.26).  The matrix cores are busy 46 % of the cycles at 2.14 GHz, where the single tokens below run
+// at 2.46, and taking out a part of any of the loop's work (products, exponentials, LDS reads, copies) shortened it in
+// proportion to that part: the readings of a part held by power, though power itself was not read.  Tiles of 64 keys
+// in two buffers and 4 waves leave room for two workgroups per CU, of which one computes while the other waits (one
+// per CU: 362 us; 8 waves: +3 %; scores a tile ahead in the same wave: +1 % or spills).  The form of 128 channels and
+// bf16 has 256 registers and 8 bytes of scratch memory, outside its loops.  8-bit cache: 353 us, as every workgroup
+// turns the codes of its tiles into bf16; heads of 64 channels: 158, as many exponentials for half the products; both:
+// 242.
 // Single tokens: memory.  64 sequences of 512 to 8192 keys: 210 us, 5.4 TB/s of the cache's bytes.
 // Trees: rows that fill no tile of 128, the pieces' unlike ends and the join.  8 trees of 7 to 48 tokens over up to 4000
-// keys, 28 heads on 4, 8-bit cache: 27 us and 5 to 6 of the join.
+// keys, 28 heads on 4, 8-bit cache: 26 us and 5 to 6 of the join.
 #include <algorithm>
 #include <cmath>
 
@@ -120,8 +126,9 @@ __device__ inline void codes_to_bf16(v4u c, v4u out[2]) {
     }
 }
 
-// A sequence's page numbers, 64 at a time in the lanes and the next 64 on their way (-1: no such page).  The first are
-// requested before the sequence's length is known, to make one trip to memory of both.
+// A sequence's page numbers, 64 at a time in the lanes and the next 64 beside them (-1: no such page).  The first are
+// requested before the sequence's length is known, to make one trip to memory of both; later ones are waited for as they
+// are read (they are checked there), one trip to memory every 64 pages.
 struct Pages {
     const int32_t* p;
     int width, n, n_pages, base, now, next;
@@ -688,7 +695,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attn_rows_kernel(AttnArgs A) {
 
 // At most 32 rows: waves take tiles of 32 keys in turn.  Rows of bf16 are copied to the other of two buffers while a tile
 // is computed; codes wait in registers, so that one buffer does, and two workgroups fit a CU (64 sequences, 64 heads, 8192
-// keys: 135 us, with two buffers 205)
+// keys: 130 us and 5 of the join, with two buffers 205 in all)
 template <int HD, bool I8, bool kRuns>
 __global__ __launch_bounds__(256, I8 || HD == 64 ? 2 : 1) void attn_keys_kernel(AttnArgs A) {
     constexpr int BK = 32, NW = 4, STEP = NW * BK, TILE = BK * HD * 2, OLD = HD + 4, BUFS = I8 ? 1 : 2;
@@ -910,6 +917,7 @@ void launch_any(const AttnArgs& A, const AttnPlan& P, bool i8, hipStream_t st) {
 //   Few rows, as many sequences and heads as run at once already: pieces for two rounds (where several workgroups share a
 //   CU: four), of 512 keys or more, so that long sequences do not end alone (64 sequences of 512 to 8000 keys, 64 heads,
 //   8-bit cache: 150 -> 135 us, with heads of 64 channels 99 -> 76; bf16, 48 sequences: 199 -> 182).
+//   (The times of a tile and of a join below are those of bf16 heads of 128 channels; other forms take the same rule.)
 //   Many rows: no more than pay.  A piece's rows are written and read back as float32 (8 bytes a channel at the copy
 //   rate), 64 keys take a workgroup 2 us where two share a CU, and the join's launch 6: pieces cost `join` each and leave
 //   whole / pieces to wait for, least at the root of their quotient.  Where every sequence has rows for all its row tiles,

@@ -12,10 +12,13 @@
 // first kernel's workgroups (one per sequence and piece of the vocabulary) each walk for themselves, from the rows'
 // gathered probabilities in LDS, then sum their piece; the second kernel finds the piece and the token in it.
 //
-// Bound by the chain of trips to memory (rows, tokens, probabilities, the last row, its sums, the piece): a chain of 5 rows
-// over 32000 entries 7.4 + 8.1 us, 32 trees of 33 rows over 131072 11.3 + 9.0 (17 MB of rows, 3 us at the copy rate).  One
-// kernel with a workgroup per sequence saves the second launch but reads a row on one CU: 11 us in place of 14 at 8000
-// entries, the same at 32000, 38 in place of 17 at 131072.
+// Bound by trips to memory that wait for each other, four in the walk (starts; rows' tokens and random numbers; their
+// probabilities; the last row) and three in the draw (sums and starts; random number and tokens; the piece), the float64
+// scans with their barriers between, and two launches: a chain of 5 rows over 32000 entries 7.4 + 8.1 us, 32 trees of 33 rows
+// over 131072 11.8 + 9.0 (17 MB of rows, 3 us at the copy rate).  One kernel with a workgroup per sequence saves the second
+// launch but reads a row on one CU: 11 us in place of 14 at 8000 entries, the same at 32000, 38 in place of 17 at 131072.
+// Trees of many rows are bound by the look for a token that a sibling has too, every pair of rows in every workgroup: 64
+// rows 8.3 us, 1024 rows 470 (32000 or 131072 entries).
 #include <algorithm>
 
 #include "qe_cache.h"
