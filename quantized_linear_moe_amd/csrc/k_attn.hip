@@ -10,7 +10,8 @@
 //
 // with c = 8 + the bits of the number of keys, so that a weight is at most 2^(8 - c) and all of them at most 1 together:
 // o stays within the values' own range, whatever it is.  The exponent s - m' is then off by up to c 2^-24 (1.3e-6 at 8192
-// keys), little beside the weights' rounding to bf16 (2^-8).
+// keys), little beside the weights' rounding to bf16 (2^-8).  At the other end, what lies below 2^-126 in the sums of o is
+// kept to steps of 2^-149, but a weight times an 8-bit value's scale is lost there.
 //
 // The weights are rounded to bf16 for the matrix cores (at most 2^-8 relative each, as the values they multiply were); l
 // is summed from the rounded weights, so that what is divided by is the sum of what was multiplied (8-bit cache: from the

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import qe_cache_oracle as C
 from test_gpu_attention import BF, DEV, Batch, _forest
 
 pytestmark = pytest.mark.gpu
@@ -97,6 +98,33 @@ def test_values_near_the_end_of_their_range(L, n, length, i8):
             if x is not None:
                 t.copy_(x)
         b.check(b.run(L))
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n,length", [(1, 300), (1, 3000), (40, 2000)])
+def test_small_values(L, n, length, i8):
+    """Weights are at least 2^-c of their row's sum where they count (c = 8 + the bits of the length).  What that adds to the
+    bound, after the division: bf16 products below 2^-126 are rounded to steps of 2^-149, 2^(c - 149) a key; with an 8-bit
+    cache a weight times its scale may vanish below 2^-126, 127 * 2^(c - 126) a key."""
+    b = Batch(L, [(n, length)], 4, 2, 64, 16, i8, seed=length)
+    if i8:
+        b.vs.mul_(1e-24)
+    else:
+        b.v.copy_((b.v.float() * 1e-34).to(BF))
+    for t, x in zip(b.tensors, (b.k, b.v, b.ks, b.vs)):
+        if x is not None:
+            t.copy_(x)
+    out = b.run(L).float().cpu().numpy().astype(np.float64)
+    seen = C.sees(n, length - n, length)
+    o, A, reach = C.attention(b.q.float().cpu().numpy(), *b.keys_of(0, length), seen, 64 ** -0.5)
+    count = seen.sum(1)[:, None, None]
+    c = 8 + length.bit_length()
+    d = 64 ** -0.5 * reach * (65 * 2.0 ** -23 + 8 * 2.0 ** -24) * 2
+    tol = 2.0 ** -8 * np.abs(o) + (1 + 2.0 ** -8) * A * (2 * 2.0 ** -8 + 2 * np.expm1(d) + 2.0 ** -20 + 2 * count * 2.0 ** -23)
+    tol = tol + count * (127 * 2.0 ** (c - 126) if i8 else 2.0 ** (c - 149))
+    assert np.all(np.abs(out - o) <= tol)
+    # the bound says something: at most 3000 * 2^(20 - 149) = 4.4e-36 beside A near 0.8e-34, with the 2^-7 of above 0.067
+    assert np.median(tol / A) < 0.1
 
 
 def _long(L, form, i8, whole, seed, hd=64, tree=False):
