@@ -431,11 +431,12 @@ int qe_add_rmsnorm(const void* x, const void* res, int32_t x_dtype, const void* 
  *   launch, so that a captured call serves every length up to them.
  *   What exceeds the bounds is left out: tokens past max_q get no row, keys past max_kv or max_pages * page_size are not
  *   seen, and the others are what they are (the new tokens' own keys are the last n of kv_len, also where some of those
- *   are left out).  Keys of pages outside the cache are not seen, and what lies in places past kv_len is not read.  What a token does not see does not reach its row, infinities and NaN included.
+ *   are left out).  Keys of pages outside the cache are not seen, and what lies in places past kv_len is not read.  What a
+ *   token does not see does not reach its row, infinities and NaN included.
  *   Products on the matrix cores with float32 sums, maxima and sums of the softmax in float32, its weights rounded to
- *   bf16 (QE_I8: after their values' scales) for the second product.  Rows of finite values are finite.  Small values keep
- *   their precision down to about 1e-35 (bf16), or 1e-23 for a head's largest (QE_I8; both up to 8192 keys).
- *   Deterministic.
+ *   bf16 (QE_I8: after their values' scales) for the second product.  Rows of finite scores and of values up to 3.3e38 are
+ *   finite.  Small values keep their precision down to about 1e-35 (bf16), or 1e-23 for a head's largest (QE_I8; both up
+ *   to 8192 keys).  Deterministic.
  *   head_dim 64 or 128 (else QE_ERR_UNSUPPORTED), n_heads a multiple of n_kv_heads, max_kv at most 2^30, scale > 0.
  *   ws: device, qe_attention_workspace_bytes bytes of the call's own arguments (0 for many calls, and for refused
  *   arguments; a smaller call may need more: one workspace for several calls has the largest of their sizes), not shared
